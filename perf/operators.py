@@ -246,7 +246,9 @@ def _plain_route(s):
     if c["train"]:
         grad = s["grad"].double()
         if c["renorm"]:
-            ds = c["scale"] / total * (grad - (grad * picked).sum(1, keepdim=True) / total)
+            # grad_j - mean as a sum of differences, which keeps its digits where the weights leave none free (k = 1)
+            differ = ((grad[:, :, None] - grad[:, None, :]) * picked[:, None, :]).sum(2)
+            ds = c["scale"] / total ** 2 * (differ + 1e-20 * grad)
         else:
             ds = c["scale"] * grad
         d = torch.zeros((T, E), dtype=torch.float64, device=x.device).scatter_(1, ids, ds)
@@ -470,8 +472,12 @@ def exact(case, seed):
             # the Jacobians, applied to the gradient one after the other
             gr = s["grad"].double()
             if case["renorm"]:
+                # d w_j / d s_l = (delta_jl S - s_j) / S^2, summed over j pair by pair
                 S = chosen.sum(1, keepdim=True) + 1e-20
-                gp = case["scale"] * (gr / S - (gr * chosen).sum(1, keepdim=True) / S ** 2)
+                gp = 1e-20 * gr
+                for j in range(k):
+                    gp = gp + chosen[:, j:j + 1] * (gr - gr[:, j:j + 1])
+                gp = case["scale"] * gp / S ** 2
             else:
                 gp = case["scale"] * gr
             full = torch.zeros_like(p).scatter_(1, ids, gp)
