@@ -412,6 +412,120 @@ DG_API dg_status pack_ue8m0_validate(const float* sf, int64_t rows, int cols, in
 DG_API dg_status quantize_fp8_1x128(const void* x, int x_f32, void* q, int32_t* sf_packed, float* sf_f32,
                                     int64_t rows, int K, void* stream);
 
+/*
+ * Routing of tokens to experts. For every token t and expert e:
+ *   s   = softmax over e of logits[t, e], or sigmoid(logits[t, e])
+ *   key = s + bias[e]                         (the bias serves the choice only)
+ * The experts form n_groups equal runs of E / n_groups; a group's score is the
+ * sum of its group_top best keys, and the top_groups best groups stay. ids are
+ * the k largest keys among their experts, in falling order, ties to the lowest
+ * index (groups likewise); weights[t, j] = scale * s[t, ids[t, j]], divided by
+ * (sum over j of s[t, ids[t, j]] + 1e-20) when renormalize = 1.
+ *   logits  : device, [T, E] bf16 (logits_f32 = 0) or fp32 (1)
+ *   bias    : device, fp32 [E], or NULL
+ *   ids     : device, int32 [T, k], written completely
+ *   weights : device, fp32 [T, k], written completely
+ *   score   : DG_SCORE_SOFTMAX or DG_SCORE_SIGMOID
+ *   group_top : 1 (a group ranks by its best expert) or 2 (by its two best)
+ * The choice is made on exact logits (no bias) or on keys good to fp64: where
+ * two keys or group scores are too close for fp32 the token is ranked again in
+ * fp64. Logits may be -inf (score 0; a row of nothing else has weights 0). A
+ * NaN key ranks below every number; a NaN or +inf logit makes the softmax
+ * weights of its row NaN. Ids are always k different experts.
+ * Limits: 1 <= k <= E <= 1024, k <= 32, n_groups <= 32 and a divisor of E,
+ * k <= top_groups * E / n_groups. Capture safe.
+ */
+#define DG_SCORE_SOFTMAX 0
+#define DG_SCORE_SIGMOID 1
+DG_API dg_status moe_route(const void* logits, int logits_f32, const float* bias, int32_t* ids, float* weights, int T,
+                           int E, int k, int score, int n_groups, int top_groups, int group_top, int renormalize,
+                           float scale, void* stream);
+
+/*
+ * Gradient of moe_route's weights with respect to the logits, for the ids it
+ * chose (the choice and the bias have no gradient).
+ *   logits, ids : as given to and written by moe_route
+ *   d_weights   : device, fp32 [T, k]
+ *   d_logits    : device, [T, E] in the logits' type, written completely; not
+ *                 the logits themselves
+ * Ids outside [0, E) count as not chosen; an expert named by two slots gets
+ * both gradients. Limits as moe_route. Capture safe.
+ */
+DG_API dg_status moe_route_backward(const void* logits, int logits_f32, const int32_t* ids, const float* d_weights,
+                                    void* d_logits, int T, int E, int k, int score, int renormalize, float scale,
+                                    void* stream);
+
+/*
+ * The rows of the experts: a stable sort of the T*k choices by expert, in the
+ * order of t*k + j within an expert.
+ *   ids      : device, int32 [T, k], the expert of every slot; a value outside
+ *              [0, G) (an expert of another device) gets no row
+ *   row_of   : device, int32 [T, k], the row of every slot, -1 for none
+ *   counts   : device, int32 [G], the choices of every expert
+ * moe_rows_contiguous lays the rows out for m_grouped_fp8_gemm_nt_contiguous:
+ * every expert starts at a multiple of 128.
+ *   m_indices : device, int32 [m_rows], the expert of every row, -1 on padding
+ *   m_rows    : rows of the layout, at least moe_rows_bound(T, k, G)
+ * moe_rows_masked lays them out for m_grouped_fp8_gemm_nt_masked: expert e
+ * owns rows e*max_m ... of [G, max_m]. Choices past max_m get row -1.
+ *   masked_m  : device, int32 [G], min(counts, max_m)
+ * Every output is written completely. Limits: k <= 32, G <= 1024, fewer than
+ * 2^31 rows. One launch, no workspace, capture safe.
+ */
+DG_API int64_t moe_rows_bound(int T, int k, int G);
+DG_API dg_status moe_rows_contiguous(const int32_t* ids, int32_t* row_of, int32_t* m_indices, int32_t* counts, int T,
+                                     int k, int G, int64_t m_rows, void* stream);
+DG_API dg_status moe_rows_masked(const int32_t* ids, int32_t* row_of, int32_t* masked_m, int32_t* counts, int T, int k,
+                                 int G, int max_m, void* stream);
+
+/*
+ * Tokens to their experts' rows, cast to E4M3: row row_of[t, j] of q and sf
+ * becomes token t, quantised once per 1x128 block.
+ *   x      : device, [T, H] bf16 (x_f32 = 0) or fp32 (1)
+ *   row_of : device, int32 [T, k]; different rows, as moe_rows_* writes them.
+ *            Slots outside [0, rows) are skipped
+ *   q      : device, E4M3 [rows, H] (a masked layout has rows = G * max_m)
+ *   sf     : device, the rows' scales: packed UE8M0, int32 [rows, ceil(H/512)]
+ *            (sf_f32 = 0), exactly as quantize_fp8_1x128 computes them, or
+ *            fp32 [rows, H/128] (sf_f32 = 1), as quantize_fp8_1x128_sf_f32
+ * Rows that no slot names (padding) are left as they were. Limits:
+ * H % 128 == 0; x and q 16-byte aligned; values finite. Capture safe. The
+ * gradient of the copies is moe_combine with weights = NULL.
+ */
+DG_API dg_status moe_dispatch_fp8(const void* x, int x_f32, const int32_t* row_of, void* q, void* sf, int sf_f32,
+                                  int64_t rows, int T, int k, int H, void* stream);
+
+/*
+ * Per-token FP8 quantiser with fp32 block scales, for the *_sf_f32 GEMMs. Per
+ * 1x128 block: amax = max(max |x|, 1e-4), scale amax / 448, codes =
+ * E4M3(x * (448 / amax)) rounded to nearest even.
+ *   x  : device, [rows, K] bf16 (x_f32 = 0) or fp32 (1)
+ *   q  : device, E4M3 [rows, K];  sf : device, fp32 [rows, K/128]
+ * A block with a non-finite value gets a non-finite scale, so the products of
+ * its row are not finite either. Limits: K % 128 == 0; x and q 16-byte
+ * aligned. Capture safe.
+ */
+DG_API dg_status quantize_fp8_1x128_sf_f32(const void* x, int x_f32, void* q, float* sf, int64_t rows, int K,
+                                           void* stream);
+
+/*
+ * The experts' rows added up into tokens:
+ *   out[t] = sum over j of weights[t, j] * y[row_of[t, j]]
+ * in fp32, in the order of j, rounded to bf16 once.
+ *   y       : device, bf16 [rows, H];  out : device, bf16 [T, H], written completely
+ *   row_of  : device, int32 [T, k]; slots outside [0, rows) are not read and add nothing
+ *   weights : device, fp32 [T, k], or NULL for ones
+ * moe_combine_backward:
+ *   d_y[row_of[t, j]]  = weights[t, j] * d_out[t]      (bf16; other rows are left as they were)
+ *   d_weights[t, j]    = <y[row_of[t, j]], d_out[t]>   (fp32; 0 for slots without a row)
+ * row_of names different rows. Outputs must not overlap inputs. Limits:
+ * H % 8 == 0, k <= 32; y, out, d_out, d_y 16-byte aligned. Capture safe.
+ */
+DG_API dg_status moe_combine(const void* y, const int32_t* row_of, const float* weights, void* out, int64_t rows, int T,
+                             int k, int H, void* stream);
+DG_API dg_status moe_combine_backward(const void* y, const int32_t* row_of, const float* weights, const void* d_out,
+                                      void* d_y, float* d_weights, int64_t rows, int T, int k, int H, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

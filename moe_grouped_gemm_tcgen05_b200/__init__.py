@@ -29,6 +29,8 @@ __all__ = [
     "fp8_gemm_nn", "fp8_gemm_tn", "fp8_gemm_tt",
     "fp8_gemm_nt_sfb_gran", "m_grouped_fp8_gemm_nt_contiguous_sfb_gran", "m_grouped_fp8_gemm_nt_masked_sfb_gran",
     "m_grouped_fp8_gemm_nt_psum",
+    "moe_route", "moe_route_backward", "moe_rows_bound", "moe_rows_contiguous", "moe_rows_masked", "moe_dispatch_fp8",
+    "moe_combine", "moe_combine_backward", "quantize_fp8_1x128_sf_f32",
     "DEVERR_TIMEOUT", "DEVERR_MIXED_EXPERT_BLOCK",
 ]
 
@@ -118,6 +120,19 @@ def load():
         L.pack_ue8m0.argtypes = [vp, vp, i64, i32, vp]
         L.pack_ue8m0_validate.restype = i32
         L.pack_ue8m0_validate.argtypes = [vp, i64, i32, vp, vp]
+        for name, args in (
+                ("moe_route", [vp, i32, vp, vp, vp] + [i32] * 8 + [ctypes.c_float, vp]),
+                ("moe_route_backward", [vp, i32, vp, vp, vp] + [i32] * 5 + [ctypes.c_float, vp]),
+                ("moe_rows_contiguous", [vp] * 4 + [i32] * 3 + [i64, vp]),
+                ("moe_rows_masked", [vp] * 4 + [i32] * 4 + [vp]),
+                ("moe_dispatch_fp8", [vp, i32, vp, vp, vp, i32, i64] + [i32] * 3 + [vp]),
+                ("quantize_fp8_1x128_sf_f32", [vp, i32, vp, vp, i64, i32, vp]),
+                ("moe_combine", [vp] * 4 + [i64] + [i32] * 3 + [vp]),
+                ("moe_combine_backward", [vp] * 6 + [i64] + [i32] * 3 + [vp])):
+            getattr(L, name).restype = i32
+            getattr(L, name).argtypes = args
+        L.moe_rows_bound.restype = i64
+        L.moe_rows_bound.argtypes = [i32, i32, i32]
         _lib = L
         return L
 
@@ -469,3 +484,209 @@ def pack_ue8m0_validate(sf, bad_count):
     rows = sf.numel() // cols if cols else 0
     _check("pack_ue8m0_validate", load().pack_ue8m0_validate(_ptr(sf), rows, cols, _ptr(bad_count), _stream()))
     return bad_count
+
+
+# ------------------------------------------------- around the experts' products
+
+_F32 = (torch.float32,)
+_LOGITS = (torch.float32, torch.bfloat16)
+_SCORES = {"softmax": 0, "sigmoid": 1}
+
+
+def _here(*tensors):
+    """All tensors live on the current device: the call runs on its stream."""
+    device = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != device:
+            raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{device}")
+
+
+def _score(score):
+    if score not in _SCORES:
+        raise ValueError(f"score={score!r}: one of {tuple(_SCORES)}")
+    return _SCORES[score]
+
+
+def _opt(t):
+    return None if t is None else _ptr(t)
+
+
+def moe_route(logits, k, *, bias=None, score="softmax", n_groups=1, top_groups=1, group_top=2, renormalize=True,
+              scale=1.0, ids=None, weights=None):
+    """Choose k of E experts for each token: logits [T, E] bf16/fp32 -> (ids int32 [T, k]
+    by falling score + bias, weights fp32 [T, k] = scale * score, divided by their sum
+    when renormalize). The choice stays within the top_groups best of n_groups equal
+    groups of experts, ranked by their group_top (1 or 2) best keys."""
+    _need(logits, "logits", _LOGITS)
+    T, E = logits.shape
+    k = int(k)
+    if bias is not None:
+        _need(bias, "bias", _F32, (E,))
+    if ids is None:
+        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+    if weights is None:
+        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+    _need(ids, "ids", _I32, (T, k))
+    _need(weights, "weights", _F32, (T, k))
+    _here(logits, bias, ids, weights)
+    _check("moe_route",
+           load().moe_route(_ptr(logits), int(logits.dtype == torch.float32), _opt(bias), _ptr(ids), _ptr(weights), T, E,
+                            k, _score(score), int(n_groups), int(top_groups), int(group_top), int(bool(renormalize)),
+                            float(scale), _stream()))
+    return ids, weights
+
+
+def moe_route_backward(logits, ids, d_weights, *, score="softmax", renormalize=True, scale=1.0, d_logits=None):
+    """Gradient of moe_route's weights: d_weights fp32 [T, k] -> d_logits [T, E] in the
+    logits' type, for the ids that moe_route chose."""
+    _need(logits, "logits", _LOGITS)
+    T, E = logits.shape
+    _need(ids, "ids", _I32)
+    if ids.dim() != 2 or ids.shape[0] != T:
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected ({T}, k)")
+    k = ids.shape[1]
+    _need(d_weights, "d_weights", _F32, (T, k))
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _need(d_logits, "d_logits", (logits.dtype,), (T, E))
+    _here(logits, ids, d_weights, d_logits)
+    _check("moe_route_backward",
+           load().moe_route_backward(_ptr(logits), int(logits.dtype == torch.float32), _ptr(ids), _ptr(d_weights),
+                                     _ptr(d_logits), T, E, k, _score(score), int(bool(renormalize)), float(scale),
+                                     _stream()))
+    return d_logits
+
+
+def moe_rows_bound(T: int, k: int, G: int) -> int:
+    """Rows that T*k choices of G experts can take in whole 128-row blocks, however they fall."""
+    return int(load().moe_rows_bound(int(T), int(k), int(G)))
+
+
+def _rows_args(ids, G, row_of, counts):
+    _need(ids, "ids", _I32)
+    if ids.dim() != 2:
+        raise ValueError(f"ids has shape {tuple(ids.shape)}, expected (T, k)")
+    if row_of is None:
+        row_of = torch.empty_like(ids)
+    if counts is None:
+        counts = torch.empty((max(int(G), 0),), dtype=torch.int32, device=ids.device)
+    _need(row_of, "row_of", _I32, ids.shape)
+    _need(counts, "counts", _I32, (G,))
+    return row_of, counts
+
+
+def moe_rows_contiguous(ids, G, *, row_of=None, m_indices=None, counts=None):
+    """Rows of the contiguous layout for the choices ids int32 [T, k] of G experts ->
+    (row_of int32 [T, k], m_indices int32 [m_rows], counts int32 [G]); m_rows is
+    moe_rows_bound(T, k, G) unless m_indices is given."""
+    row_of, counts = _rows_args(ids, G, row_of, counts)
+    T, k = ids.shape
+    if m_indices is None:
+        m_indices = torch.empty((moe_rows_bound(T, k, G),), dtype=torch.int32, device=ids.device)
+    _need(m_indices, "m_indices", _I32, (m_indices.numel(),))
+    _here(ids, row_of, m_indices, counts)
+    _check("moe_rows_contiguous",
+           load().moe_rows_contiguous(_ptr(ids), _ptr(row_of), _ptr(m_indices), _ptr(counts), T, k, int(G),
+                                      m_indices.numel(), _stream()))
+    return row_of, m_indices, counts
+
+
+def moe_rows_masked(ids, G, max_m, *, row_of=None, masked_m=None, counts=None):
+    """Rows of the masked layout [G, max_m] for the choices ids int32 [T, k] ->
+    (row_of int32 [T, k], -1 past max_m; masked_m int32 [G]; counts int32 [G])."""
+    row_of, counts = _rows_args(ids, G, row_of, counts)
+    T, k = ids.shape
+    if masked_m is None:
+        masked_m = torch.empty((G,), dtype=torch.int32, device=ids.device)
+    _need(masked_m, "masked_m", _I32, (G,))
+    _here(ids, row_of, masked_m, counts)
+    _check("moe_rows_masked",
+           load().moe_rows_masked(_ptr(ids), _ptr(row_of), _ptr(masked_m), _ptr(counts), T, k, int(G), int(max_m),
+                                  _stream()))
+    return row_of, masked_m, counts
+
+
+def _row_count(t, H, name):
+    """Rows of [rows, H] or of the masked layout [G, max_m, H]."""
+    if t.dim() not in (2, 3) or t.shape[-1] != H:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected (rows, {H}) or (G, max_m, {H})")
+    return t.shape[0] if t.dim() == 2 else t.shape[0] * t.shape[1]
+
+
+def moe_dispatch_fp8(x, row_of, q, sf):
+    """Write token t of x [T, H] bf16/fp32, cast to E4M3, to the rows row_of[t] of q
+    ([rows, H] or [G, max_m, H]) and its scales to sf: int32 [..., ceil(H/512)] packed
+    UE8M0, or fp32 [..., H/128]. Other rows are left as they were."""
+    _need(x, "x", _LOGITS)
+    T, H = x.shape
+    _need(row_of, "row_of", _I32)
+    if row_of.dim() != 2 or row_of.shape[0] != T:
+        raise ValueError(f"row_of has shape {tuple(row_of.shape)}, expected ({T}, k)")
+    _need(q, "q", _FP8)
+    rows = _row_count(q, H, "q")
+    _need(sf, "sf", (torch.int32, torch.float32))
+    sf_f32 = sf.dtype == torch.float32
+    _need(sf, "sf", (sf.dtype,), (*q.shape[:-1], H // BLOCK if sf_f32 else _kp(H)))
+    _here(x, row_of, q, sf)
+    _check("moe_dispatch_fp8",
+           load().moe_dispatch_fp8(_ptr(x), int(x.dtype == torch.float32), _ptr(row_of), _ptr(q), _ptr(sf), int(sf_f32),
+                                   rows, T, row_of.shape[1], H, _stream()))
+    return q, sf
+
+
+def quantize_fp8_1x128_sf_f32(x, q=None, sf=None):
+    """x [rows, K] bf16/fp32 -> (q E4M3 as uint8 [rows, K], sf fp32 [rows, K/128] = amax / 448)."""
+    _need(x, "x", _LOGITS)
+    rows, K = x.shape
+    if q is None:
+        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+    if sf is None:
+        sf = torch.empty((rows, K // BLOCK), dtype=torch.float32, device=x.device)
+    _need(q, "q", _FP8, (rows, K))
+    _need(sf, "sf", _F32, (rows, K // BLOCK))
+    _here(x, q, sf)
+    _check("quantize_fp8_1x128_sf_f32",
+           load().quantize_fp8_1x128_sf_f32(_ptr(x), int(x.dtype == torch.float32), _ptr(q), _ptr(sf), rows, K,
+                                            _stream()))
+    return q, sf
+
+
+def _combine_args(y, row_of, weights):
+    _need(y, "y", _BF16)
+    if y.dim() not in (2, 3):
+        raise ValueError(f"y has shape {tuple(y.shape)}, expected (rows, H) or (G, max_m, H)")
+    H = y.shape[-1]
+    _need(row_of, "row_of", _I32)
+    if row_of.dim() != 2:
+        raise ValueError(f"row_of has shape {tuple(row_of.shape)}, expected (T, k)")
+    if weights is not None:
+        _need(weights, "weights", _F32, row_of.shape)
+    return _row_count(y, H, "y"), *row_of.shape, H
+
+
+def moe_combine(y, row_of, weights=None, out=None):
+    """out [T, H] bf16 = sum over j of weights[t, j] * y[row_of[t, j]] for y [rows, H] or
+    [G, max_m, H] bf16; slots with row -1 add nothing; weights None means ones."""
+    rows, T, k, H = _combine_args(y, row_of, weights)
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+    _need(out, "out", _BF16, (T, H))
+    _here(y, row_of, weights, out)
+    _check("moe_combine", load().moe_combine(_ptr(y), _ptr(row_of), _opt(weights), _ptr(out), rows, T, k, H, _stream()))
+    return out
+
+
+def moe_combine_backward(y, row_of, weights, d_out, d_y, d_weights=None):
+    """Gradients of moe_combine: d_y[row_of[t, j]] = weights[t, j] * d_out[t] (other rows are
+    left as they were) and d_weights[t, j] = <y[row_of[t, j]], d_out[t]> fp32."""
+    rows, T, k, H = _combine_args(y, row_of, weights)
+    _need(d_out, "d_out", _BF16, (T, H))
+    _need(d_y, "d_y", _BF16, y.shape)
+    if d_weights is None:
+        d_weights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    _need(d_weights, "d_weights", _F32, (T, k))
+    _here(y, row_of, weights, d_out, d_y, d_weights)
+    _check("moe_combine_backward",
+           load().moe_combine_backward(_ptr(y), _ptr(row_of), _opt(weights), _ptr(d_out), _ptr(d_y), _ptr(d_weights),
+                                       rows, T, k, H, _stream()))
+    return d_y, d_weights

@@ -22,6 +22,7 @@
 
 #include "dgb200.h"
 #include "gemm_kernel.cuh"
+#include "host.h"
 #include "pack_kernel.cuh"
 
 // Device status word (DG_DEVERR_* bits). One per device that loads the library.
@@ -800,6 +801,24 @@ dg_status psum_nt(const void* a, const int32_t* sfa, const void* b, const int32_
 }
 
 }  // namespace
+
+namespace dg {
+
+dg_status host_device(HostDevice* out) {
+    DeviceState* st = nullptr;
+    const dg_status s = current_device(&st);
+    if (s != DG_OK) return s;
+    *out = {static_cast<int>(st - g_dev), st->sms, st->status};
+    return DG_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 host_tensor_map_encode() { return g_encode; }
+uint64_t host_wait_limit_ns() { return g_wait_limit_ns.load(); }
+int host_test_mode() { return g_test_mode.load(); }
+bool host_pdl() { return g_pdl; }
+bool host_log() { return g_log; }
+
+}  // namespace dg
 
 extern "C" {
 

@@ -1,0 +1,852 @@
+// Kernels around the experts' products: routing (with its gradient), the rows
+// of each expert, the tokens' copies in those rows cast to E4M3, and the sum of
+// the experts' rows back into tokens (with its gradients).
+//
+// All of them move bytes: a few operations per value read. Every sum has one
+// fixed order, so repeated calls give identical bits; no kernel uses atomics
+// whose order could change a result.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "ptx.cuh"
+
+namespace dg {
+
+constexpr int MOE_MAX_EXPERTS = 1024;
+constexpr int MOE_MAX_TOPK = 32;       // one lane of a warp per chosen expert
+constexpr int MOE_MAX_EXPERT_GROUPS = 32;
+constexpr float ROUTE_EPS = 1e-20f;    // added to the sum that weights are divided by
+
+// ---------------------------------------------------------------- routing ----
+//
+// Per token: s = sigmoid(x) or softmax(x); key = s + bias; the groups of
+// experts are ranked by the sum of their group_top best keys and the
+// top_groups best stay; ids are the k largest keys left, ties to the lowest
+// index; weights are scale * s[ids], divided by their sum when renormalised.
+//
+// One warp per token, expert e = lane * V + i in register i of its lane, so
+// the lowest lane and register of equal keys is the lowest index, and a group
+// is a run of lanes whenever its size is V times a power of two.
+//
+// Two keys can lie closer than fp32 resolves (16384 tokens of 256 experts
+// hold a few such pairs), and the choice must not depend on the rounding of a
+// fast exponential. So keys are computed in fp32 (error below ROUTE_TOL / 4),
+// and a token where two neighbours of the sorted choice, or two groups, lie
+// within ROUTE_TOL is ranked again in fp64. Without a bias the logits
+// themselves rank like the scores and no token needs that.
+
+constexpr float ROUTE_TOL = 4e-6f;
+
+struct RouteParams {
+    const void* logits;   // [T, E]
+    const float* bias;    // [E] or null
+    int32_t* ids;         // [T, k]
+    float* weights;       // [T, k]
+    int tokens, experts, k;
+    int groups, top_groups, group_top;
+    int softmax, renorm;
+    float scale;
+};
+
+template <bool F32>
+__device__ __forceinline__ float load_logit(const void* x, size_t i) {
+    if constexpr (F32) return __ldg(static_cast<const float*>(x) + i);
+    else return __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t*>(x) + i)) << 16);
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+
+// Keys rank as themselves with NaN below every number and -0 equal to +0.
+template <typename Key>
+__device__ __forceinline__ Key rank_key(Key v) {
+    return v != v ? static_cast<Key>(-INFINITY) : v + static_cast<Key>(0);
+}
+
+// fp32 keys as unsigned integers of the same order (never 0, which marks "none left").
+__device__ __forceinline__ uint32_t ordered_bits(float v) {
+    const uint32_t u = __float_as_uint(v);
+    return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
+}
+
+__device__ __forceinline__ float from_ordered_bits(uint32_t u) {
+    return __uint_as_float((u & 0x80000000u) ? (u ^ 0x80000000u) : ~u);
+}
+
+template <typename Key>
+__device__ __forceinline__ bool near_keys(Key a, Key b) {
+    // equal infinities differ by NaN: not near, their order goes by the index
+    const Key d = a - b;
+    const Key m = fmax(static_cast<Key>(1), fmax(fabs(a), fabs(b)));
+    return fabs(d) <= static_cast<Key>(ROUTE_TOL) * m;
+}
+
+// The groups that stay, as a bit mask over groups. `near` is set when two
+// groups' scores lie within the tolerance of each other.
+template <int V, typename Key>
+__device__ __forceinline__ uint32_t route_groups(const RouteParams& p, const Key (&key)[V], int lane, bool& near) {
+    const int size = p.experts / p.groups;
+    const int run = size / V;  // lanes of a group, when its experts fill whole lanes
+    Key score = static_cast<Key>(-INFINITY);  // lane g: the score of group g
+    if (size % V == 0 && (run & (run - 1)) == 0) {
+        Key b1 = static_cast<Key>(-INFINITY), b2 = b1;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            b2 = fmax(b2, fmin(b1, key[i]));
+            b1 = fmax(b1, key[i]);
+        }
+        for (int o = 1; o < run; o <<= 1) {
+            const Key c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+            b2 = fmax(fmin(b1, c1), fmax(b2, c2));
+            b1 = fmax(b1, c1);
+        }
+        const Key s = rank_key(p.group_top == 2 ? b1 + b2 : b1);
+        const Key mine = __shfl_sync(0xffffffffu, s, (lane * run) & 31);
+        if (lane < p.groups) score = mine;
+    } else {
+        for (int g = 0; g < p.groups; ++g) {
+            Key b1 = static_cast<Key>(-INFINITY), b2 = b1;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const int e = lane * V + i;
+                if (e >= g * size && e < (g + 1) * size) {
+                    b2 = fmax(b2, fmin(b1, key[i]));
+                    b1 = fmax(b1, key[i]);
+                }
+            }
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const Key c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+                b2 = fmax(fmin(b1, c1), fmax(b2, c2));
+                b1 = fmax(b1, c1);
+            }
+            if (lane == g) score = rank_key(p.group_top == 2 ? b1 + b2 : b1);
+        }
+    }
+    int rank = 0;
+    near = false;
+    for (int h = 0; h < p.groups; ++h) {
+        const Key other = __shfl_sync(0xffffffffu, score, h);
+        rank += (other > score || (other == score && h < lane)) ? 1 : 0;
+        near |= h != lane && lane < p.groups && near_keys(other, score);
+    }
+    near = __any_sync(0xffffffffu, near) != 0;
+    return __ballot_sync(0xffffffffu, lane < p.groups && rank < p.top_groups);
+}
+
+// Experts of this lane that may be chosen, as a bit mask over its registers.
+template <int V>
+__device__ __forceinline__ uint32_t route_alive(const RouteParams& p, uint32_t kept, int lane) {
+    const int size = p.experts / p.groups;
+    uint32_t alive = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        if (e < p.experts && (p.top_groups == p.groups || (kept >> (e / size)) & 1u)) alive |= 1u << i;
+    }
+    return alive;
+}
+
+// Scores of this lane's experts in fp64 (the second look at close choices).
+template <int V, bool F32>
+__device__ __noinline__ void route_scores64(const RouteParams& p, size_t row, int lane, double (&s)[V]) {
+    double m = -INFINITY;
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        s[i] = e < p.experts ? static_cast<double>(load_logit<F32>(p.logits, row + e)) : -INFINITY;
+        m = fmax(m, s[i]);
+    }
+    if (!p.softmax) {
+        for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-s[i]));
+        return;
+    }
+    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (m == -INFINITY) m = 0.0;
+    double sum = 0.0;
+    for (int i = 0; i < V; ++i) {
+        s[i] = exp(s[i] - m);
+        sum += s[i];
+    }
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
+    for (int i = 0; i < V; ++i) s[i] *= inv;
+}
+
+// The choice again with fp64 keys: lane j < k returns its expert.
+template <int V, bool F32>
+__device__ __noinline__ int route_choose64(const RouteParams& p, size_t row, int lane) {
+    double s[V], key[V];
+    route_scores64<V, F32>(p, row, lane, s);
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        if (p.bias != nullptr && e < p.experts) s[i] += static_cast<double>(__ldg(p.bias + e));
+        s[i] = e < p.experts ? rank_key(s[i]) : -INFINITY;
+        // without a bias the experts are ranked by their logits
+        key[i] = s[i];
+        if (p.bias == nullptr && e < p.experts) key[i] = rank_key(static_cast<double>(load_logit<F32>(p.logits, row + e)));
+    }
+    uint32_t kept = 0;
+    bool near;
+    if (p.top_groups < p.groups) kept = route_groups<V, double>(p, s, lane, near);
+    uint32_t alive = route_alive<V>(p, kept, lane);
+    int mine = 0;
+    for (int j = 0; j < p.k; ++j) {
+        double best = -INFINITY;
+        int e = MOE_MAX_EXPERTS;
+        for (int i = 0; i < V; ++i)
+            if (((alive >> i) & 1u) && (e == MOE_MAX_EXPERTS || key[i] > best)) {
+                best = key[i];
+                e = lane * V + i;
+            }
+        for (int o = 16; o > 0; o >>= 1) {
+            const double b = __shfl_xor_sync(0xffffffffu, best, o);
+            const int f = __shfl_xor_sync(0xffffffffu, e, o);
+            if (f != MOE_MAX_EXPERTS && (e == MOE_MAX_EXPERTS || b > best || (b == best && f < e))) {
+                best = b;
+                e = f;
+            }
+        }
+        if (lane == j) mine = e;
+        if (e / V == lane) alive &= ~(1u << (e % V));
+    }
+    return mine;
+}
+
+constexpr int ROUTE_THREADS = 256;
+
+template <int V, bool F32>
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RouteParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = static_cast<int>(threadIdx.x & 31u);
+    const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+    if (t >= p.tokens) return;  // whole warps
+    const size_t row = static_cast<size_t>(t) * p.experts;
+    float x[V];
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = lane * V + i;
+        x[i] = e < p.experts ? load_logit<F32>(p.logits, row + e) : -INFINITY;
+        top = fmaxf(top, x[i]);
+    }
+    // softmax: the row's maximum (0 where every logit is -inf) and 1 / sum (0 then)
+    float inv = 1.f;
+    if (p.softmax) {
+        top = warp_max(top);
+        if (top == -INFINITY) top = 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += lane * V + i < p.experts ? expf(x[i] - top) : 0.f;
+        sum = warp_sum(sum);
+        inv = sum == 0.f ? 0.f : 1.f / sum;
+    }
+    // Keys: scores plus bias, or without a bias the logits, which rank alike.
+    // The groups' scores need the scores themselves when they are sums.
+    const bool grouped = p.top_groups < p.groups;
+    const bool by_score = p.bias != nullptr;
+    float key[V];
+    uint32_t kept = 0;
+    bool close = false;
+    if (by_score || (grouped && p.group_top == 2)) {
+        float s[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            const float ex = __expf(p.softmax ? x[i] - top : -x[i]);
+            float v = p.softmax ? ex * inv : __fdividef(1.f, 1.f + ex);
+            // (1 + ex infinite or past __fdividef's range: the score is 0)
+            if (!p.softmax && x[i] < -80.f) v = 0.f;
+            if (by_score && e < p.experts) v += __ldg(p.bias + e);
+            s[i] = e < p.experts ? rank_key(v) : -INFINITY;
+            key[i] = by_score ? s[i] : rank_key(x[i]);
+        }
+        if (grouped) kept = route_groups<V, float>(p, s, lane, close);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) key[i] = rank_key(x[i]);
+        bool near;  // the groups' best logits are exact
+        if (grouped) kept = route_groups<V, float>(p, key, lane, near);
+    }
+    int mine = 0;
+    if (!close) {
+        uint32_t alive = route_alive<V>(p, kept, lane);
+        uint32_t best = 0, before = 0;
+        int at = 0;
+        auto rescan = [&]() {
+            best = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                const uint32_t u = (alive >> i) & 1u ? ordered_bits(key[i]) : 0u;
+                if (u > best) {
+                    best = u;
+                    at = i;
+                }
+            }
+        };
+        rescan();
+        // one round more than k where the last choice may be a close one
+        const int rounds = p.k + (by_score ? 1 : 0);
+        for (int j = 0; j < rounds; ++j) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
+            if (m == 0) break;  // nothing left (k is every expert there is)
+            if (by_score && j > 0) close |= near_keys(from_ordered_bits(before), from_ordered_bits(m));
+            before = m;
+            const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, best == m))) - 1;
+            const int e = __shfl_sync(0xffffffffu, lane * V + at, src);
+            if (lane == j) mine = e;
+            if (lane == src) {
+                alive &= ~(1u << at);
+                rescan();
+            }
+        }
+    }
+    if (close) mine = route_choose64<V, F32>(p, row, lane);
+    // weights, from the chosen experts' logits
+    float s = 0.f;
+    if (lane < p.k) {
+        const float v = load_logit<F32>(p.logits, row + mine);
+        s = p.softmax ? expf(v - top) * inv : 1.f / (1.f + expf(-v));
+    }
+    float w = p.scale * s;
+    if (p.renorm) w /= warp_sum(lane < p.k ? s : 0.f) + ROUTE_EPS;
+    if (lane < p.k) {
+        p.ids[static_cast<size_t>(t) * p.k + lane] = mine;
+        p.weights[static_cast<size_t>(t) * p.k + lane] = w;
+    }
+}
+
+// Gradient of the weights with respect to the logits, for given ids:
+//   renormalised  ds_j = scale / S^2 * (sum_l (g_j - g_l) s_l + g_j eps),  S = sum s_l + eps
+//   otherwise     ds_j = scale * g_j
+//   sigmoid       dx_j = ds_j s_j (1 - s_j), 0 elsewhere
+//   softmax       dx_i = s_i (ds_i - c),  c = sum_j ds_j s_j (scale * mean(g) * eps / S when renormalised)
+// The differences g_j - g_l keep the digits that g_j - mean(g) would cancel.
+// One warp per token; lane j < k holds choice j. Ids outside [0, E) count as
+// not chosen; an expert named twice gets both slots' gradients.
+struct RouteBackwardParams {
+    const void* logits;      // [T, E]
+    const int32_t* ids;      // [T, k]
+    const float* d_weights;  // [T, k]
+    void* d_logits;          // [T, E], the logits' type
+    int tokens, experts, k;
+    int softmax, renorm;
+    float scale;
+};
+
+template <bool F32>
+__device__ __forceinline__ void store_logit(void* x, size_t i, float v) {
+    if constexpr (F32) static_cast<float*>(x)[i] = v;
+    else static_cast<__nv_bfloat16*>(x)[i] = __float2bfloat16_rn(v);
+}
+
+template <int V, bool F32>
+__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(const RouteBackwardParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = static_cast<int>(threadIdx.x & 31u);
+    const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
+    if (t >= p.tokens) return;
+    const size_t row = static_cast<size_t>(t) * p.experts;
+    // expert e = 32 i + lane: a row is read and written in whole lines
+    float s[V];
+    float top = 0.f, inv = 0.f;
+    if (p.softmax) {
+        top = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int e = 32 * i + lane;
+            s[i] = e < p.experts ? load_logit<F32>(p.logits, row + e) : -INFINITY;
+            top = fmaxf(top, s[i]);
+        }
+        top = warp_max(top);
+        if (top == -INFINITY) top = 0.f;
+        float sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = 32 * i + lane < p.experts ? expf(s[i] - top) : 0.f;
+            sum += s[i];
+        }
+        sum = warp_sum(sum);
+        inv = sum == 0.f ? 0.f : 1.f / sum;
+    }
+    int id = -1;
+    float g = 0.f, sj = 0.f, not_sj = 0.f;
+    if (lane < p.k) {
+        id = __ldg(p.ids + static_cast<size_t>(t) * p.k + lane);
+        if (id < 0 || id >= p.experts) id = -1;
+    }
+    if (id >= 0) {
+        g = __ldg(p.d_weights + static_cast<size_t>(t) * p.k + lane);
+        const float x = load_logit<F32>(p.logits, row + id);
+        if (p.softmax) {
+            sj = expf(x - top) * inv;
+        } else {
+            sj = 1.f / (1.f + expf(-x));
+            not_sj = 1.f / (1.f + expf(x));
+        }
+    }
+    float ds = p.scale * g, c;
+    if (p.renorm) {
+        const float total = warp_sum(sj) + ROUTE_EPS;
+        float diff = 0.f;
+        for (int l = 0; l < p.k; ++l) {
+            const float gl = __shfl_sync(0xffffffffu, g, l), sl = __shfl_sync(0xffffffffu, sj, l);
+            diff += (g - gl) * sl;
+        }
+        ds = id >= 0 ? p.scale * ((diff + g * ROUTE_EPS) / total) / total : 0.f;
+        c = p.scale * (warp_sum(g * sj) / total) * (ROUTE_EPS / total);
+    } else {
+        c = warp_sum(ds * sj);
+    }
+    float both = 0.f;  // every slot that names this lane's expert
+    for (int l = 0; l < p.k; ++l) {
+        const float dl = __shfl_sync(0xffffffffu, ds, l);
+        const int il = __shfl_sync(0xffffffffu, id, l);
+        if (il == id) both += dl;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = 32 * i + lane;
+        if (e < p.experts) store_logit<F32>(p.d_logits, row + e, p.softmax ? -c * (s[i] * inv) : 0.f);
+    }
+    __syncwarp();  // the chosen experts' entries are written again, after the row
+    if (id >= 0) store_logit<F32>(p.d_logits, row + id, p.softmax ? sj * (both - c) : both * sj * not_sj);
+}
+
+// ------------------------------------------------------- rows of the experts ----
+//
+// A stable counting sort of the T*k choices by expert: choice i = t*k + j gets
+// row base[e] + (choices of expert e before i), where base[e] is the sum of
+// the earlier experts' rows rounded up to whole 128-row blocks (contiguous
+// form), or e * max_m (masked form; ranks at or past max_m get row -1).
+//
+// One cluster of up to 8 CTAs does it in one launch, with no workspace: every
+// warp owns a run of choices and a row of counters in shared memory, counts
+// it, the counters are turned into first rows by a scan over warps, CTAs
+// (through distributed shared memory) and experts, and the run is walked a
+// second time to hand the rows out. Ranks inside 32 choices come from
+// match_any. Bound by latency: the run of a warp is walked 32 choices a step.
+
+constexpr int ROWS_THREADS = 1024;
+constexpr int ROWS_WARPS = ROWS_THREADS / 32;
+constexpr int ROWS_MAX_CLUSTER = 8;
+
+struct RowsParams {
+    const int32_t* ids;   // [n]; outside [0, G): no row
+    int32_t* row_of;      // [n]
+    int32_t* meta;        // m_indices [m_cap] (contiguous) or masked_m [G] (masked)
+    int32_t* counts;      // [G]
+    int n, groups;
+    int m_cap;            // contiguous: rows of m_indices
+    int max_m;            // masked: rows of an expert; 0 = contiguous
+};
+
+// dynamic shared memory: [ROWS_WARPS][G] counters, [G] this CTA's choices, [G] all choices, [G + 1] first rows
+__host__ __device__ constexpr int rows_smem_bytes(int groups) { return (ROWS_WARPS * groups + 3 * groups + 1) * 4; }
+
+__device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
+    int v;
+    asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+__global__ void __launch_bounds__(ROWS_THREADS, 1) moe_rows_kernel(const RowsParams p) {
+    extern __shared__ int rows_smem[];
+    __shared__ int warp_totals[ROWS_WARPS];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int G = p.groups;
+    int* hist = rows_smem;                    // [warp][G]
+    int* cta_total = hist + ROWS_WARPS * G;   // [G], read by the other CTAs too
+    int* all_total = cta_total + G;           // [G]
+    int* first = all_total + G;               // [G + 1]
+    const int tid = static_cast<int>(threadIdx.x);
+    const int lane = tid & 31, warp = tid >> 5;
+    const int ctas = static_cast<int>(gridDim.x), rank = static_cast<int>(blockIdx.x);  // one cluster
+    for (int i = tid; i < ROWS_WARPS * G; i += ROWS_THREADS) hist[i] = 0;
+    __syncthreads();
+
+    // this warp's run of choices, in whole steps of 32
+    const int warps = ctas * ROWS_WARPS;
+    const int64_t steps = (static_cast<int64_t>(p.n) + 31) / 32;
+    const int64_t me = rank * ROWS_WARPS + warp;
+    const int begin = static_cast<int>(steps * me / warps * 32);
+    const int end = static_cast<int>(min(static_cast<int64_t>(p.n), steps * (me + 1) / warps * 32));
+    int* mine = hist + warp * G;
+    for (int i = begin + lane; i < end; i += 32) {
+        const int e = __ldg(p.ids + i);
+        if (e >= 0 && e < G) atomicAdd(mine + e, 1);  // whole numbers: any order gives the same count
+    }
+    __syncthreads();
+
+    // counters -> choices of the expert in earlier warps of this CTA; thread e owns expert e
+    if (tid < G) {
+        int run = 0;
+#pragma unroll 8
+        for (int w = 0; w < ROWS_WARPS; ++w) {
+            const int c = hist[w * G + tid];
+            hist[w * G + tid] = run;
+            run += c;
+        }
+        cta_total[tid] = run;
+    }
+    cluster_sync();
+    int before = 0, total = 0;
+    if (tid < G) {
+        const uint32_t at = smem_u32(cta_total + tid);
+        for (int r = 0; r < ctas; ++r) {
+            const int c = ld_cluster_s32(mapa_shared(at, static_cast<uint32_t>(r)));
+            if (r < rank) before += c;
+            total += c;
+        }
+    }
+    // first rows: an exclusive scan of the experts' whole blocks
+    const int rows = (tid < G && p.max_m == 0) ? (total + 127) / 128 * 128 : 0;
+    int incl = rows;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_totals[warp] = incl;
+    __syncthreads();
+    if (warp == 0) {
+        int v = warp_totals[lane];
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += u;
+        }
+        warp_totals[lane] = v;
+    }
+    __syncthreads();
+    if (tid < G) {
+        const int base = p.max_m ? tid * p.max_m : (warp ? warp_totals[warp - 1] : 0) + incl - rows;
+        first[tid] = base;
+        if (tid == G - 1) first[G] = base + rows;
+#pragma unroll 8
+        for (int w = 0; w < ROWS_WARPS; ++w) hist[w * G + tid] += base + before;
+        if (rank == 0) {
+            p.counts[tid] = total;
+            if (p.max_m) p.meta[tid] = min(total, p.max_m);
+        }
+        all_total[tid] = total;
+    }
+    __syncthreads();
+    for (int i0 = begin; i0 < end; i0 += 32) {
+        const int i = i0 + lane;
+        int e = i < end ? __ldg(p.ids + i) : -1;
+        if (e < 0 || e >= G) e = -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, e);
+        const int at = e >= 0 ? mine[e] : 0;
+        __syncwarp();
+        const int row = at + __popc(same & ((1u << lane) - 1u));
+        if (e >= 0 && lane == 31 - __clz(static_cast<int>(same))) mine[e] = row + 1;
+        __syncwarp();
+        if (i < end) {
+            const bool fits = e >= 0 && (p.max_m == 0 || row - e * p.max_m < p.max_m);
+            p.row_of[i] = fits ? row : -1;
+        }
+    }
+    if (p.max_m == 0) {
+        // the expert of every row of every 128-row block; -1 on padding rows and past the last block
+        const int blocks = (p.m_cap + 127) / 128;
+        for (int b = rank * ROWS_WARPS + warp; b < blocks; b += warps) {
+            const int r0 = b * 128;
+            int e = -1, filled = 0;
+            if (r0 < first[G]) {
+                int lo = 0, hi = G - 1;  // the last expert whose first row is at or before r0
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) / 2;
+                    if (first[mid] <= r0) lo = mid;
+                    else hi = mid - 1;
+                }
+                e = lo;
+                filled = first[e] + all_total[e];
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int r = r0 + 32 * j + lane;
+                if (r < p.m_cap) p.meta[r] = r < filled ? e : -1;
+            }
+        }
+    }
+    cluster_sync();  // no CTA leaves while a peer may read its totals
+}
+
+// ---------------------------------------------------------------- dispatch ----
+//
+// q[row_of[t, j]] = E4M3(x[t] / s), with one scale s per 128 values: a power of
+// two, packed as UE8M0 (the rule of quantize_fp8_1x128), or amax / 448 in
+// fp32. A token is read and cast once and its codes are written k times, so
+// the traffic is the floor: T*H values in, T*k*H codes out.
+//
+// A warp handles four 128-value blocks of a token (one packed scale word):
+// lane l takes 16 values of block l / 8, whose amax is a maximum over 8 lanes.
+
+constexpr int DISPATCH_THREADS = 256;
+
+struct DispatchParams {
+    const void* x;          // [T, H] bf16 or fp32
+    const int32_t* row_of;  // [T, k], or null: row t (k = 1)
+    uint4* q;               // [rows, H] E4M3
+    void* sf;               // [rows, ceil(H/512)] int32 (UE8M0) or [rows, H/128] fp32
+    int64_t rows;
+    int tokens, k;
+    int kb, kp;             // H / 128, ceil(H / 512)
+};
+
+template <bool IN_F32>
+__device__ __forceinline__ void load16(const void* x, int64_t at, float (&v)[16]) {
+    if constexpr (IN_F32) {
+        const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 f = __ldg(src + i);
+            v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+        }
+    } else {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(x) + at);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const uint4 u = __ldg(src + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                v[8 * i + 2 * j] = __uint_as_float(w[j] << 16);
+                v[8 * i + 2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+            }
+        }
+    }
+}
+
+template <bool IN_F32, bool SF_F32>
+__global__ void __launch_bounds__(DISPATCH_THREADS) moe_dispatch_fp8_kernel(const DispatchParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = static_cast<int>(threadIdx.x & 31u);
+    const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
+    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
+    const int64_t words = static_cast<int64_t>(p.tokens) * p.kp;
+    for (int64_t i = warp0; i < words; i += nwarps) {
+        const int t = static_cast<int>(i / p.kp);
+        const int word = static_cast<int>(i - static_cast<int64_t>(t) * p.kp);
+        const int block = 4 * word + (lane >> 3);
+        const bool there = block < p.kb;
+        float v[16];
+        if (there) {
+            load16<IN_F32>(p.x, (static_cast<int64_t>(t) * p.kb + block) * 128 + 16 * (lane & 7), v);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = 0.f;
+        }
+        uint32_t m = __float_as_uint(1e-4f);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+#pragma unroll
+        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        float scale, inv;
+        uint32_t byte = 0;
+        if constexpr (SF_F32) {
+            scale = __uint_as_float(m) / 448.f;
+            inv = 448.f / __uint_as_float(m);
+        } else {
+            const int e = static_cast<int>((m >> 23) & 0xFFu) - 127 - 8 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+            byte = there ? static_cast<uint32_t>(127 + e) : 0u;
+            scale = 0.f;
+            inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        }
+        uint32_t c[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            c[j] = e4m3x2_rn(v[4 * j + 1] * inv, v[4 * j] * inv) |
+                   (e4m3x2_rn(v[4 * j + 3] * inv, v[4 * j + 2] * inv) << 16);
+        const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
+        // the four blocks' bytes meet in lane 0's word
+        uint32_t packed = 0;
+        if constexpr (!SF_F32) {
+            packed = byte << (8 * (lane >> 3));
+            packed |= __shfl_xor_sync(0xffffffffu, packed, 8);
+            packed |= __shfl_xor_sync(0xffffffffu, packed, 16);
+        }
+        for (int j = 0; j < p.k; ++j) {
+            const int64_t r = p.row_of != nullptr ? __ldg(p.row_of + static_cast<int64_t>(t) * p.k + j) : t;
+            if (r < 0 || r >= p.rows) continue;  // the same in every lane
+            if (there) p.q[(r * p.kb + block) * 8 + (lane & 7)] = codes;
+            if constexpr (SF_F32) {
+                if (there && (lane & 7) == 0) static_cast<float*>(p.sf)[r * p.kb + block] = scale;
+            } else {
+                if (lane == 0) static_cast<uint32_t*>(p.sf)[r * p.kp + word] = packed;
+            }
+        }
+    }
+}
+
+// ----------------------------------------------------------------- combine ----
+//
+// out[t] = sum_j w[t, j] y[row_of[t, j]], in fp32 in the order of j, rounded to
+// bf16 once. Slots without a row (outside [0, rows)) are not read and add
+// nothing. One thread per eight columns of a token, up to eight rows' loads in
+// flight.
+
+constexpr int COMBINE_THREADS = 256;
+constexpr int COMBINE_BATCH = 8;
+
+struct CombineParams {
+    const uint4* y;         // [rows, H] bf16
+    const int32_t* row_of;  // [T, k]
+    const float* w;         // [T, k], or null: ones
+    uint4* out;             // [T, H] bf16
+    int64_t rows;
+    int tokens, k;
+    int vecs;               // H / 8
+};
+
+__device__ __forceinline__ void bf16x8_to_f32(const uint4& u, float (&v)[8]) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        v[2 * j] = __uint_as_float(w[j] << 16);
+        v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ uint4 f32_to_bf16x8(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * j], v[2 * j + 1]);
+        w[j] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const CombineParams p) {
+    griddep_launch_dependents();
+    griddep_wait();
+    const int64_t n = static_cast<int64_t>(p.tokens) * p.vecs;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
+    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
+        const int t = static_cast<int>(i / p.vecs);
+        const int c = static_cast<int>(i - static_cast<int64_t>(t) * p.vecs);
+        float acc[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+        for (int j0 = 0; j0 < p.k; j0 += COMBINE_BATCH) {
+            uint4 u[COMBINE_BATCH];
+            float w[COMBINE_BATCH];
+            bool live[COMBINE_BATCH];
+#pragma unroll
+            for (int j = 0; j < COMBINE_BATCH; ++j) {
+                live[j] = false;
+                if (j0 + j >= p.k) continue;
+                const int64_t at = static_cast<int64_t>(t) * p.k + j0 + j;
+                const int64_t r = __ldg(p.row_of + at);
+                live[j] = r >= 0 && r < p.rows;
+                if (!live[j]) continue;
+                w[j] = p.w != nullptr ? __ldg(p.w + at) : 1.f;
+                u[j] = __ldg(p.y + r * p.vecs + c);
+            }
+#pragma unroll
+            for (int j = 0; j < COMBINE_BATCH; ++j) {
+                if (!live[j]) continue;
+                float v[8];
+                bf16x8_to_f32(u[j], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], v[e], acc[e]);
+            }
+        }
+        p.out[i] = f32_to_bf16x8(acc);
+    }
+}
+
+// Gradients of combine: d_y[row_of[t, j]] = w[t, j] d_out[t] (bf16) and
+// d_w[t, j] = <y[row_of[t, j]], d_out[t]> (fp32). Slots without a row get
+// d_w = 0; rows that no slot names are left as they were.
+// One CTA per token: its threads cover the columns and add up eight slots at a
+// time; the sums over threads go by warps and then in warp order.
+
+struct CombineBackwardParams {
+    const uint4* y;         // [rows, H] bf16
+    const int32_t* row_of;  // [T, k]
+    const float* w;         // [T, k], or null: ones
+    const uint4* d_out;     // [T, H] bf16
+    uint4* d_y;             // [rows, H] bf16
+    float* d_w;             // [T, k]
+    int64_t rows;
+    int tokens, k;
+    int vecs;
+};
+
+__global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_backward_kernel(const CombineBackwardParams p) {
+    __shared__ float part[COMBINE_THREADS / 32][COMBINE_BATCH];
+    griddep_launch_dependents();
+    griddep_wait();
+    const int t = static_cast<int>(blockIdx.x);
+    const int lane = static_cast<int>(threadIdx.x & 31u), warp = static_cast<int>(threadIdx.x >> 5);
+    const int warps = static_cast<int>(blockDim.x >> 5);
+    const int64_t slot0 = static_cast<int64_t>(t) * p.k;
+    for (int j0 = 0; j0 < p.k; j0 += COMBINE_BATCH) {
+        int64_t r[COMBINE_BATCH];
+        float w[COMBINE_BATCH], dot[COMBINE_BATCH];
+#pragma unroll
+        for (int j = 0; j < COMBINE_BATCH; ++j) {
+            dot[j] = 0.f;
+            r[j] = -1;
+            w[j] = 0.f;
+            if (j0 + j >= p.k) continue;
+            r[j] = __ldg(p.row_of + slot0 + j0 + j);
+            if (r[j] >= p.rows) r[j] = -1;
+            if (r[j] >= 0) w[j] = p.w != nullptr ? __ldg(p.w + slot0 + j0 + j) : 1.f;
+        }
+        for (int c = static_cast<int>(threadIdx.x); c < p.vecs; c += static_cast<int>(blockDim.x)) {
+            uint4 u[COMBINE_BATCH];
+#pragma unroll
+            for (int j = 0; j < COMBINE_BATCH; ++j)
+                if (r[j] >= 0) u[j] = __ldg(p.y + r[j] * p.vecs + c);
+            float d[8];
+            bf16x8_to_f32(__ldg(p.d_out + static_cast<int64_t>(t) * p.vecs + c), d);
+#pragma unroll
+            for (int j = 0; j < COMBINE_BATCH; ++j) {
+                if (r[j] < 0) continue;
+                float v[8], o[8];
+                bf16x8_to_f32(u[j], v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    dot[j] = fmaf(v[e], d[e], dot[j]);
+                    o[e] = w[j] * d[e];
+                }
+                p.d_y[r[j] * p.vecs + c] = f32_to_bf16x8(o);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < COMBINE_BATCH; ++j) {
+            const float s = warp_sum(dot[j]);
+            if (lane == 0) part[warp][j] = s;
+        }
+        __syncthreads();
+        const int j = static_cast<int>(threadIdx.x);
+        if (j < COMBINE_BATCH && j0 + j < p.k) {
+            float s = 0.f;
+            for (int i = 0; i < warps; ++i) s += part[i][j];
+            p.d_w[slot0 + j0 + j] = s;
+        }
+        __syncthreads();
+    }
+}
+
+}  // namespace dg

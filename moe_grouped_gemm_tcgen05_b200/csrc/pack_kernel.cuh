@@ -108,12 +108,6 @@ struct QuantRaw {
     }
 };
 
-__device__ __forceinline__ uint32_t e4m3x2_rn(float hi, float lo) {
-    uint16_t r;
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-    return r;  // e4m3(hi) in bits 15..8, e4m3(lo) in bits 7..0
-}
-
 template <bool IN_F32>
 __global__ void __launch_bounds__(QUANT_THREADS, QUANT_BLOCKS_PER_SM)
 quantize_fp8_1x128_kernel(const void* __restrict__ x, uint32_t* __restrict__ q,

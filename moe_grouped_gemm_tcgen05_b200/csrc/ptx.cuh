@@ -42,6 +42,13 @@ __device__ __forceinline__ void griddep_launch_dependents() {
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// Two fp32 values to E4M3, rounded to nearest even, clamped to +-448.
+__device__ __forceinline__ uint32_t e4m3x2_rn(float hi, float lo) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;  // e4m3(hi) in bits 15..8, e4m3(lo) in bits 7..0
+}
+
 // ---------------------------------------------------------------- mbarrier --
 
 __device__ __forceinline__ void mbar_init(uint64_t* bar, uint32_t count) {

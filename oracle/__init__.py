@@ -19,6 +19,8 @@ ue8m0  -- UE8M0 scale bytes: decode, the capture-safe pack of fp32 scales
 gemm   -- dequantise-and-multiply references for the dense NT GEMM and the
           contiguous / masked / psum_m-driven M-grouped GEMMs, and the BF16
           masked grouped GEMM
+moe    -- routing with its gradient, the experts' rows, dispatch and combine
+          (with gradients), and the products with fp32 block scales
 
 Sources (web pages about DeepGEMM):
   [P1] "DeepGEMM CUDA Graph Compatibility for Masked Grouped GEMMs:
@@ -57,3 +59,4 @@ from .gemm import (  # noqa: F401
     m_grouped_bf16_gemm_nt_masked,
     m_grouped_bf16_gemm_nt_masked_sampled,
 )
+from . import moe  # noqa: F401
