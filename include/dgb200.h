@@ -413,6 +413,39 @@ DG_API dg_status quantize_fp8_1x128(const void* x, int x_f32, void* q, int32_t* 
                                     int64_t rows, int K, void* stream);
 
 /*
+ * FP8 NT GEMMs whose block scales are fp32 numbers of any value (a checkpoint's
+ * weight scales need not be powers of two), in the dense, contiguous and masked
+ * forms:
+ *   D[m, n] = (C[m, n] +) sum over 128-K blocks of
+ *             sfa[m, kb] * sfb[.., kb] * sum over k in kb of A[m, k] * B[n, k]
+ *   a, b, d, m_indices, masked_m : as in fp8_gemm_nt_acc,
+ *         m_grouped_fp8_gemm_nt_contiguous and m_grouped_fp8_gemm_nt_masked
+ *   sfa : device, fp32 [rows of a, K/128]  (masked: [G, max_m, K/128])
+ *   sfb : device, fp32 [ceil(N/128), K/128] per weight matrix; dense calls with
+ *         sfb_gran_n = 1: [N, K/128], one row per row of B. sfb_gran_n is 128
+ *         or 1, anything else returns DG_ERR_INVALID_ARG
+ *   c, out_f32 : as in fp8_gemm_nt_acc (c may equal d, and must not overlap it otherwise)
+ * Every block is accumulated in fp32 by the tensor core, scaled and added in
+ * fp32; D is rounded once. Untouched rows, DG_DEVERR_MIXED_EXPERT_BLOCK,
+ * limits, errors, bounded waits and capture safety are those of the calls
+ * named. quantize_fp8_1x128_sf_f32 makes A and sfa.
+ * The gradients of the dense product Y = X . W^T are the same call: dX = dY . W
+ * takes W's codes and its 128x128 scales transposed as B, and dW = dY^T . X
+ * takes both operands transposed and quantised along the tokens (sfb_gran_n =
+ * 1), with an fp32 D that C accumulates into.
+ * dgb200_set_block_n, _set_cta_group and _set_splits apply; a combination that
+ * is not built returns DG_ERR_UNSUPPORTED.
+ */
+DG_API dg_status fp8_gemm_nt_sf_f32(const void* a, const float* sfa, const void* b, const float* sfb, int sfb_gran_n,
+                                    const void* c, void* d, int M, int N, int K, int out_f32, void* stream);
+DG_API dg_status m_grouped_fp8_gemm_nt_contiguous_sf_f32(const void* a, const float* sfa, const void* b,
+                                                         const float* sfb, void* d, const int32_t* m_indices,
+                                                         int M_total, int N, int K, int G, void* stream);
+DG_API dg_status m_grouped_fp8_gemm_nt_masked_sf_f32(const void* a, const float* sfa, const void* b, const float* sfb,
+                                                     void* d, const int32_t* masked_m, int G, int max_m, int N, int K,
+                                                     void* stream);
+
+/*
  * Routing of tokens to experts. For every token t and expert e:
  *   s   = softmax over e of logits[t, e], or sigmoid(logits[t, e])
  *   key = s + bias[e]                         (the bias serves the choice only)

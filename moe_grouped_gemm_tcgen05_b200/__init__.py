@@ -31,6 +31,7 @@ __all__ = [
     "m_grouped_fp8_gemm_nt_psum",
     "moe_route", "moe_route_backward", "moe_rows_bound", "moe_rows_contiguous", "moe_rows_masked", "moe_dispatch_fp8",
     "moe_combine", "moe_combine_backward", "quantize_fp8_1x128_sf_f32",
+    "fp8_gemm_nt_sf_f32", "m_grouped_fp8_gemm_nt_contiguous_sf_f32", "m_grouped_fp8_gemm_nt_masked_sf_f32",
     "DEVERR_TIMEOUT", "DEVERR_MIXED_EXPERT_BLOCK",
 ]
 
@@ -127,6 +128,9 @@ def load():
                 ("moe_rows_masked", [vp] * 4 + [i32] * 4 + [vp]),
                 ("moe_dispatch_fp8", [vp, i32, vp, vp, vp, i32, i64] + [i32] * 3 + [vp]),
                 ("quantize_fp8_1x128_sf_f32", [vp, i32, vp, vp, i64, i32, vp]),
+                ("fp8_gemm_nt_sf_f32", [vp] * 4 + [i32, vp, vp] + [i32] * 4 + [vp]),
+                ("m_grouped_fp8_gemm_nt_contiguous_sf_f32", [vp] * 6 + [i32] * 4 + [vp]),
+                ("m_grouped_fp8_gemm_nt_masked_sf_f32", [vp] * 6 + [i32] * 4 + [vp]),
                 ("moe_combine", [vp] * 4 + [i64] + [i32] * 3 + [vp]),
                 ("moe_combine_backward", [vp] * 6 + [i64] + [i32] * 3 + [vp])):
             getattr(L, name).restype = i32
@@ -690,3 +694,64 @@ def moe_combine_backward(y, row_of, weights, d_out, d_y, d_weights=None):
            load().moe_combine_backward(_ptr(y), _ptr(row_of), _opt(weights), _ptr(d_out), _ptr(d_y), _ptr(d_weights),
                                        rows, T, k, H, _stream()))
     return d_y, d_weights
+
+
+# ------------------------------------------------- products with fp32 block scales
+
+def fp8_gemm_nt_sf_f32(a, sfa, b, sfb, d, c=None, sfb_gran_n: int = BLOCK):
+    """d[M, N] = c + (a . sfa) @ (b . sfb)^T with fp32 scales of any value: sfa [M, K/128];
+    sfb [ceil(N/128), K/128] (sfb_gran_n=128) or [N, K/128] (sfb_gran_n=1). d is bf16 or
+    fp32; c (optional) has d's dtype and may be d itself (in-place accumulation)."""
+    _need(a, "a", _FP8)
+    M, K = a.shape
+    _need(b, "b", _FP8)
+    N = b.shape[0]
+    _need(b, "b", _FP8, (N, K))
+    _need(sfa, "sfa", _F32, (M, K // BLOCK))
+    _need(sfb, "sfb", _F32, (_sfb_rows(N, sfb_gran_n), K // BLOCK))
+    _need(d, "d", (torch.bfloat16, torch.float32), (M, N))
+    if c is not None:
+        _need(c, "c", (d.dtype,), (M, N))
+    _here(a, sfa, b, sfb, d, c)
+    _check("fp8_gemm_nt_sf_f32",
+           load().fp8_gemm_nt_sf_f32(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), int(sfb_gran_n), _opt(c), _ptr(d), M, N, K,
+                                     int(d.dtype == torch.float32), _stream()))
+    return d
+
+
+def m_grouped_fp8_gemm_nt_contiguous_sf_f32(a, sfa, b, sfb, d, m_indices):
+    """m_grouped_fp8_gemm_nt_contiguous with fp32 scales: sfa [M_total, K/128],
+    sfb [G, ceil(N/128), K/128]."""
+    _need(a, "a", _FP8)
+    M_total, K = a.shape
+    _need(b, "b", _FP8)
+    G, N = b.shape[0], b.shape[1]
+    _need(b, "b", _FP8, (G, N, K))
+    _need(sfa, "sfa", _F32, (M_total, K // BLOCK))
+    _need(sfb, "sfb", _F32, (G, _sfb_rows(N, BLOCK), K // BLOCK))
+    _need(d, "d", _BF16, (M_total, N))
+    _need(m_indices, "m_indices", _I32, (M_total,))
+    _here(a, sfa, b, sfb, d, m_indices)
+    _check("m_grouped_fp8_gemm_nt_contiguous_sf_f32",
+           load().m_grouped_fp8_gemm_nt_contiguous_sf_f32(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d),
+                                                          _ptr(m_indices), M_total, N, K, G, _stream()))
+    return d
+
+
+def m_grouped_fp8_gemm_nt_masked_sf_f32(a, sfa, b, sfb, d, masked_m):
+    """m_grouped_fp8_gemm_nt_masked with fp32 scales: sfa [G, max_m, K/128],
+    sfb [G, ceil(N/128), K/128]."""
+    _need(a, "a", _FP8)
+    G, max_m, K = a.shape
+    _need(b, "b", _FP8)
+    N = b.shape[1]
+    _need(b, "b", _FP8, (G, N, K))
+    _need(sfa, "sfa", _F32, (G, max_m, K // BLOCK))
+    _need(sfb, "sfb", _F32, (G, _sfb_rows(N, BLOCK), K // BLOCK))
+    _need(d, "d", _BF16, (G, max_m, N))
+    _need(masked_m, "masked_m", _I32, (G,))
+    _here(a, sfa, b, sfb, d, masked_m)
+    _check("m_grouped_fp8_gemm_nt_masked_sf_f32",
+           load().m_grouped_fp8_gemm_nt_masked_sf_f32(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(masked_m),
+                                                      G, max_m, N, K, _stream()))
+    return d

@@ -236,7 +236,7 @@ dg_status setup_device(int dev, DeviceState& st) {
     void* status = nullptr;
     if (cudaGetSymbolAddress(&status, g_dg_device_status) != cudaSuccess) return DG_ERR_CUDA;
     st.status = static_cast<uint32_t*>(status);
-    return DG_OK;
+    return dg::setup_sf_f32(dev, st.sms);
 }
 
 // Set up device `dev`, which must be the current device. Allocates nothing.
@@ -812,7 +812,18 @@ dg_status host_device(HostDevice* out) {
     return DG_OK;
 }
 
-PFN_cuTensorMapEncodeTiled_v12000 host_tensor_map_encode() { return g_encode; }
+bool host_encode_kmajor(CUtensorMap* map, const void* base, int rank, int64_t k, int64_t rows, int64_t mats,
+                        int box_rows) {
+    return encode_kmajor(map, base, rank, static_cast<uint64_t>(k), static_cast<uint64_t>(rows),
+                         static_cast<uint64_t>(mats), static_cast<uint32_t>(box_rows), kE4M3);
+}
+
+void host_forced_tile(int* block_n, int* cta_group, int* splits) {
+    *block_n = g_force_bn.load();
+    *cta_group = g_force_cg.load();
+    *splits = g_force_splits.load();
+}
+
 uint64_t host_wait_limit_ns() { return g_wait_limit_ns.load(); }
 int host_test_mode() { return g_test_mode.load(); }
 bool host_pdl() { return g_pdl; }

@@ -396,6 +396,113 @@ __device__ __forceinline__ bool next_tile(const GemmParams& p, const int* s_pref
     }
 }
 
+// The tile scheduler's tables in shared memory, from the device metadata.
+// Masked: s_mm[g] = clamped masked_m, s_prefix = tile prefix sums. psum_m:
+// s_mm = the groups' first rows. Contiguous: s_prefix[b] = expert of 128-row
+// block b, when the blocks fit. All THREADS threads of the CTA; the caller
+// synchronises before the tables are read.
+template <int KIND, int THREADS>
+__device__ __forceinline__ void prepare_schedule(const GemmParams& p, int* s_prefix, int* s_mm, uint32_t warp,
+                                                 uint32_t lane) {
+    if constexpr (KIND == kMasked) {
+        // masked_m clamped to [0, max_m]
+        for (int g = threadIdx.x; g < p.groups; g += THREADS) s_mm[g] = min(max(__ldg(p.meta + g), 0), p.rows);
+        __syncthreads();
+    }
+    if constexpr (KIND == kPsum) {
+        // first row of every group: s_mm[0] = 0, s_mm[g + 1] = end of group g =
+        // min(max(0, psum_m[0..g]), M_total), a running max so that no row
+        // belongs to two groups (warp 0: per-lane maxima, then a max-scan)
+        if (warp == 0) {
+            const int per = (p.groups + 31) / 32;
+            const int g0 = static_cast<int>(lane) * per;
+            int mx = 0;
+            for (int i = 0; i < per; ++i)
+                if (g0 + i < p.groups) mx = max(mx, __ldg(p.meta + g0 + i));
+            int incl = mx;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= static_cast<uint32_t>(o)) incl = max(incl, v);
+            }
+            int run = __shfl_up_sync(0xffffffffu, incl, 1);
+            if (lane == 0) run = 0;
+            for (int i = 0; i < per; ++i) {
+                const int g = g0 + i;
+                if (g < p.groups) {
+                    run = max(run, __ldg(p.meta + g));
+                    s_mm[g + 1] = min(run, p.rows);
+                }
+            }
+            if (lane == 0) s_mm[0] = 0;
+        }
+        __syncthreads();
+    }
+    if constexpr (KIND == kMasked || KIND == kPsum) {
+        // tile prefix over groups (warp 0 scans)
+        if (warp == 0) {
+            const int per = (p.groups + 31) / 32;
+            const int g0 = static_cast<int>(lane) * per;
+            int sum = 0;
+            for (int i = 0; i < per; ++i) {
+                const int g = g0 + i;
+                if (g < p.groups) sum += ((group_rows<KIND>(s_mm, g) + BM - 1) / BM) * p.num_n_blocks;
+            }
+            int incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= static_cast<uint32_t>(o)) incl += v;
+            }
+            int run = incl - sum;
+            for (int i = 0; i < per; ++i) {
+                const int g = g0 + i;
+                if (g < p.groups) {
+                    s_prefix[g] = run;
+                    run += ((group_rows<KIND>(s_mm, g) + BM - 1) / BM) * p.num_n_blocks;
+                }
+            }
+            if (lane == 31) s_prefix[p.groups] = incl;
+        }
+    }
+    if constexpr (KIND == kContiguous) {
+        // expert of every 128-row block = largest valid index among its rows
+        // (-1: padding only), kept in shared memory when the blocks fit
+        // Each warp takes 8 blocks per round (lane l: rows 4l..4l+3 of each,
+        // one 16-byte load when m_indices allows) and reduces each block.
+        const int nblk = (p.rows + BM - 1) / BM;
+        if (nblk <= MAX_CACHED_BLOCKS) {
+            constexpr int kWarps = THREADS / 32;
+            const bool vec = (reinterpret_cast<uintptr_t>(p.meta) & 15) == 0;
+            auto expert_or_none = [&](int id) { return (id >= 0 && id < p.groups) ? id : -1; };
+            for (int b0 = static_cast<int>(warp) * 8; b0 < nblk; b0 += kWarps * 8) {
+                int best[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    int m = -1;
+                    const int r0 = (b0 + u) * BM + 4 * static_cast<int>(lane);
+                    if (b0 + u < nblk) {
+                        if (vec && r0 + 3 < p.rows) {
+                            const int4 v = __ldg(reinterpret_cast<const int4*>(p.meta + r0));
+                            m = max(max(expert_or_none(v.x), expert_or_none(v.y)),
+                                    max(expert_or_none(v.z), expert_or_none(v.w)));
+                        } else {
+                            for (int j = 0; j < 4; ++j)
+                                if (r0 + j < p.rows) m = max(m, expert_or_none(__ldg(p.meta + r0 + j)));
+                        }
+                    }
+                    best[u] = m;
+                }
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const int m = __reduce_max_sync(0xffffffffu, best[u]);
+                    if (lane == 0 && b0 + u < nblk) s_prefix[b0 + u] = m;
+                }
+            }
+        }
+    }
+}
+
 // Group of four K-blocks visited at step gi of tile t. Rotating the start by
 // the tile index makes CTAs that share an A or B tile (and run in lockstep)
 // touch its K-blocks at different times, so only one of them waits for DRAM
@@ -754,9 +861,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(cbar + 4);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     volatile int* s_last = reinterpret_cast<volatile int*>(s_tmem + 2);  // split-K: this unit reduces
-    int* s_prefix = reinterpret_cast<int*>(s_tmem + 4);             // [groups + 1] (masked, psum_m)
+    int* s_prefix = reinterpret_cast<int*>(s_tmem + 4);             // [groups + 1] (masked, psum_m), [128-row blocks] (contiguous)
     int* s_mm = s_prefix + MAX_MASKED_GROUPS + 4;                   // [groups] (masked), [groups + 1] (psum_m)
-    int* s_bexp = s_prefix;                                          // [128-row blocks] (contiguous)
 
     const uint32_t warp = threadIdx.x / 32;
     const uint32_t lane = lane_id();
@@ -816,103 +922,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
     // scheduled right away (it waits for this grid in turn).
     griddep_launch_dependents();
     griddep_wait();
-    if constexpr (KIND == kMasked) {
-        // masked_m clamped to [0, max_m]
-        for (int g = threadIdx.x; g < p.groups; g += NUM_THREADS) s_mm[g] = min(max(__ldg(p.meta + g), 0), p.rows);
-        __syncthreads();
-    }
-    if constexpr (KIND == kPsum) {
-        // first row of every group: s_mm[0] = 0, s_mm[g + 1] = end of group g =
-        // min(max(0, psum_m[0..g]), M_total), a running max so that no row
-        // belongs to two groups (warp 0: per-lane maxima, then a max-scan)
-        if (warp == 0) {
-            const int per = (p.groups + 31) / 32;
-            const int g0 = static_cast<int>(lane) * per;
-            int mx = 0;
-            for (int i = 0; i < per; ++i)
-                if (g0 + i < p.groups) mx = max(mx, __ldg(p.meta + g0 + i));
-            int incl = mx;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= static_cast<uint32_t>(o)) incl = max(incl, v);
-            }
-            int run = __shfl_up_sync(0xffffffffu, incl, 1);
-            if (lane == 0) run = 0;
-            for (int i = 0; i < per; ++i) {
-                const int g = g0 + i;
-                if (g < p.groups) {
-                    run = max(run, __ldg(p.meta + g));
-                    s_mm[g + 1] = min(run, p.rows);
-                }
-            }
-            if (lane == 0) s_mm[0] = 0;
-        }
-        __syncthreads();
-    }
-    if constexpr (KIND == kMasked || KIND == kPsum) {
-        // tile prefix over groups (warp 0 scans)
-        if (warp == 0) {
-            const int per = (p.groups + 31) / 32;
-            const int g0 = static_cast<int>(lane) * per;
-            int sum = 0;
-            for (int i = 0; i < per; ++i) {
-                const int g = g0 + i;
-                if (g < p.groups) sum += ((group_rows<KIND>(s_mm, g) + BM - 1) / BM) * p.num_n_blocks;
-            }
-            int incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= static_cast<uint32_t>(o)) incl += v;
-            }
-            int run = incl - sum;
-            for (int i = 0; i < per; ++i) {
-                const int g = g0 + i;
-                if (g < p.groups) {
-                    s_prefix[g] = run;
-                    run += ((group_rows<KIND>(s_mm, g) + BM - 1) / BM) * p.num_n_blocks;
-                }
-            }
-            if (lane == 31) s_prefix[p.groups] = incl;
-        }
-    }
-    if constexpr (KIND == kContiguous) {
-        // expert of every 128-row block = largest valid index among its rows
-        // (-1: padding only), kept in shared memory when the blocks fit
-        // Each warp takes 8 blocks per round (lane l: rows 4l..4l+3 of each,
-        // one 16-byte load when m_indices allows) and reduces each block.
-        const int nblk = (p.rows + BM - 1) / BM;
-        if (nblk <= MAX_CACHED_BLOCKS) {
-            constexpr int kWarps = NUM_THREADS / 32;
-            const bool vec = (reinterpret_cast<uintptr_t>(p.meta) & 15) == 0;
-            auto expert_or_none = [&](int id) { return (id >= 0 && id < p.groups) ? id : -1; };
-            for (int b0 = static_cast<int>(warp) * 8; b0 < nblk; b0 += kWarps * 8) {
-                int best[8];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    int m = -1;
-                    const int r0 = (b0 + u) * BM + 4 * static_cast<int>(lane);
-                    if (b0 + u < nblk) {
-                        if (vec && r0 + 3 < p.rows) {
-                            const int4 v = __ldg(reinterpret_cast<const int4*>(p.meta + r0));
-                            m = max(max(expert_or_none(v.x), expert_or_none(v.y)),
-                                    max(expert_or_none(v.z), expert_or_none(v.w)));
-                        } else {
-                            for (int j = 0; j < 4; ++j)
-                                if (r0 + j < p.rows) m = max(m, expert_or_none(__ldg(p.meta + r0 + j)));
-                        }
-                    }
-                    best[u] = m;
-                }
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int m = __reduce_max_sync(0xffffffffu, best[u]);
-                    if (lane == 0 && b0 + u < nblk) s_bexp[b0 + u] = m;
-                }
-            }
-        }
-    }
+    prepare_schedule<KIND, NUM_THREADS>(p, s_prefix, s_mm, warp, lane);
     tc_fence_before();
     __syncthreads();
     // every CTA's barriers exist before any cross-CTA signal (pairs, cluster split-K)

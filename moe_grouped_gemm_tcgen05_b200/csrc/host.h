@@ -4,7 +4,6 @@
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
 
 #include <cstdint>
 
@@ -20,11 +19,19 @@ struct HostDevice {
 
 // The current device, set up on its first use (dgb200.cu).
 dg_status host_device(HostDevice* out);
-PFN_cuTensorMapEncodeTiled_v12000 host_tensor_map_encode();
+// Tensor map of a K-major E4M3 operand [mats, rows, k] in boxes of 128 bytes of K by box_rows rows.
+bool host_encode_kmajor(CUtensorMap* map, const void* base, int rank, int64_t k, int64_t rows, int64_t mats,
+                        int box_rows);
+// The overrides of dgb200_set_block_n, _set_cta_group and _set_splits (0: none).
+void host_forced_tile(int* block_n, int* cta_group, int* splits);
 uint64_t host_wait_limit_ns();  // bound of every wait inside a kernel
 int host_test_mode();           // dgb200_set_test_hooks
 bool host_pdl();                // DGB200_PDL
 bool host_log();                // DGB200_LOG
+
+// Kernel attributes and co-resident units of the GEMMs with fp32 scales on the
+// current device (gemm_sf_f32.cu); part of the device's set-up.
+dg_status setup_sf_f32(int device, int sms);
 
 inline bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

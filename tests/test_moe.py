@@ -172,6 +172,32 @@ def test_combine_refusals(lib):
     assert back(dy=VP(0x20008)) == 2 and back(dw=VP(0x20002)) == 2
 
 
+def test_sf_f32_gemm_refusals(lib):
+    def dense(a=GOOD, sfa=GOOD, b=GOOD, sfb=GOOD, gran=128, c=None, d=GOOD, M=64, N=128, K=256, f32=0):
+        return lib.fp8_gemm_nt_sf_f32(a, sfa, b, sfb, gran, c, d, M, N, K, f32, None)
+
+    def cont(a=GOOD, sfa=GOOD, b=GOOD, sfb=GOOD, d=GOOD, m=GOOD, M=64, N=128, K=256, G=2):
+        return lib.m_grouped_fp8_gemm_nt_contiguous_sf_f32(a, sfa, b, sfb, d, m, M, N, K, G, None)
+
+    def masked(a=GOOD, sfa=GOOD, b=GOOD, sfb=GOOD, d=GOOD, m=GOOD, M=64, N=128, K=256, G=2):
+        return lib.m_grouped_fp8_gemm_nt_masked_sf_f32(a, sfa, b, sfb, d, m, G, M, N, K, None)
+
+    for call in (dense, cont, masked):
+        for kw in (dict(a=None), dict(sfa=None), dict(b=None), dict(sfb=None), dict(d=None), dict(M=0), dict(N=0),
+                   dict(K=0), dict(K=100), dict(N=12)):
+            assert call(**kw) == 1, kw
+        assert call(K=(1 << 20) + 128) == 3
+        for name in ("a", "b", "d"):
+            assert call(**{name: VP(0x10008)}) == 2
+        assert call(sfa=VP(0x10002)) == 2 and call(sfb=VP(0x10001)) == 2
+    for kw in (dict(gran=64), dict(gran=0), dict(f32=2)):
+        assert dense(**kw) == 1
+    assert dense(c=VP(0x10008)) == 2
+    for call in (cont, masked):
+        assert call(m=None) == 1 and call(G=0) == 1 and call(m=VP(0x10002)) == 2
+    assert masked(G=1025) == 3
+
+
 def test_binding_refusals():
     """The binding takes CUDA tensors of the right types only, and names the argument."""
     x, ids = torch.zeros((4, 256)), torch.zeros((4, 2), dtype=torch.int32)
