@@ -30,11 +30,11 @@ Entry entry() {
 }
 
 const Entry kEntries[] = {
-    entry<128, dg::kDense, 1, 1, false>(),      entry<192, dg::kDense, 2, 2, false>(),
-    entry<224, dg::kDense, 2, 2, false>(),     entry<256, dg::kDense, 2, 2, false>(),
-    entry<128, dg::kDense, 1, 1, true>(),       entry<256, dg::kDense, 2, 2, true>(),
-    entry<128, dg::kContiguous, 1, 1, false>(), entry<224, dg::kContiguous, 2, 2, false>(),
-    entry<256, dg::kContiguous, 2, 2, false>(),
+    entry<128, dg::kDense, 1, 1, false>(),      entry<192, dg::kDense, 2, 1, false>(),
+    entry<224, dg::kDense, 2, 1, false>(),     entry<256, dg::kDense, 2, 1, false>(),
+    entry<128, dg::kDense, 1, 1, true>(),       entry<256, dg::kDense, 2, 1, true>(),
+    entry<128, dg::kContiguous, 1, 1, false>(), entry<224, dg::kContiguous, 2, 1, false>(),
+    entry<256, dg::kContiguous, 2, 1, false>(),
     entry<128, dg::kMasked, 1, 1, false>(),
 };
 constexpr int kNumEntries = sizeof(kEntries) / sizeof(kEntries[0]);

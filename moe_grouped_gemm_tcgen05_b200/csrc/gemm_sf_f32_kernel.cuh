@@ -23,8 +23,8 @@
 //               the epilogue (56 + 2 x 224 of the launch's 3 x 168 per lane)
 //   warps 4..   epilogue. Warp w reads TMEM lanes 32 (w % 4) .. + 31 (a row per
 //               lane) and owns half of the tile's columns, CW = BN / 2, whose
-//               accumulators stay in its registers over the whole K loop. 16
-//               columns are read from TMEM while the 16 before are added.
+//               accumulators stay in its registers over the whole K loop. 32
+//               columns are read from TMEM while the 32 before are added.
 // The tile's columns are NSUB sub-tiles with rings of TMEM buffers and barriers
 // of their own, so that a sub-tile's buffer is refilled NBUF blocks later while
 // the other sub-tiles' MMAs run.
@@ -89,6 +89,18 @@ __device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16]) {
                  :: "memory");
 }
 
+// Scale loads that stay where they are written: left to itself the compiler moves
+// them down to their use, four K-blocks later, and the warp waits for L2 there.
+__device__ __forceinline__ float ld_scale(const float* p) {
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void ld_scale4(const float* p, float (&v)[4]) {
+    asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
+}
+
 // Registers of the calling warpgroup from here on (per thread).
 template <int N>
 __device__ __forceinline__ void registers_inc() {
@@ -97,26 +109,6 @@ __device__ __forceinline__ void registers_inc() {
 template <int N>
 __device__ __forceinline__ void registers_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// Two fp32 values in one 64-bit register, and the packed FMA and product on them.
-__device__ __forceinline__ uint64_t pack_f32x2(uint32_t lo, uint32_t hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(lo), "r"(hi));
-    return r;
-}
-__device__ __forceinline__ void unpack_f32x2(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
 }
 
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
@@ -178,7 +170,7 @@ struct StoreRows {
 // lanes take the 64 bytes of a row. (Row-wise 16-byte stores straight from the
 // registers touch 32 rows per instruction and slow the operand loads.)
 template <int CW, int STG_ROW>
-__device__ __forceinline__ void store_rows(const GemmParams& p, const uint64_t (&acc)[CW / 2], const StoreRows& to,
+__device__ __forceinline__ void store_rows(const GemmParams& p, const float (&acc)[CW], const StoreRows& to,
                                            int col0, uint8_t* stg, int lane) {
     const int sub = lane >> 2, piece = lane & 3;
     if (p.c == nullptr && !p.out_f32) {
@@ -191,9 +183,7 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const uint64_t (
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    float lo, hi;
-                    unpack_f32x2(acc[u / 2 + 4 * q + i], lo, hi);
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(acc[u + 8 * q + 2 * i], acc[u + 8 * q + 2 * i + 1]);
                     w[i] = *reinterpret_cast<const uint32_t*>(&b);
                 }
                 *reinterpret_cast<uint4*>(stg + lane * STG_ROW + 16 * q) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -217,10 +207,9 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const uint64_t (
         __syncwarp();
 #pragma unroll
         for (int q = 0; q < pieces; ++q) {
-            float f[4];
-            unpack_f32x2(acc[u / 2 + 2 * q], f[0], f[1]);
-            unpack_f32x2(acc[u / 2 + 2 * q + 1], f[2], f[3]);
-            *reinterpret_cast<float4*>(stg + lane * STG_ROW + 16 * q) = make_float4(f[0], f[1], f[2], f[3]);
+            const int j = u + 4 * q;
+            *reinterpret_cast<float4*>(stg + lane * STG_ROW + 16 * q) =
+                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
         }
         __syncwarp();
         const int col = col0 + u + 4 * piece;
@@ -472,20 +461,19 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             // columns of this warp before the next 128-column block
             [[maybe_unused]] const int first_cols = 128 - (col0 & 127);
 
-            uint64_t acc[CW / 2];
+            float acc[CW];
 #pragma unroll
-            for (int i = 0; i < CW / 2; ++i) acc[i] = 0;
+            for (int i = 0; i < CW; ++i) acc[i] = 0.f;
 
             // scales of four K-blocks, the next four in flight
             float na[4], nb[4];
             [[maybe_unused]] float nb1[4];
             auto load4 = [&](const float* row, int kb0, bool vec, float (&v)[4]) {
                 if (vec) {
-                    const float4 f = __ldg(reinterpret_cast<const float4*>(row + kb0));
-                    v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+                    ld_scale4(row + kb0, v);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = __ldg(row + min(kb0 + i, p.kb - 1));
+                    for (int i = 0; i < 4; ++i) v[i] = ld_scale(row + min(kb0 + i, p.kb - 1));
                 }
             };
             // ROWB: the four warps of a column group share its CW columns' scales:
@@ -502,7 +490,25 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                     if constexpr (kTwoBlocks) load4(sb1, 4 * kg, p.sfb_vec4 != 0, nb1);
                 }
             };
+            // The block products, 16 columns at a time in two sets of registers: a
+            // chunk's read is issued before the chunk before it is added, across
+            // blocks too, so that the reads pass under the FMAs. 8 warps read and
+            // add 128 columns each in ~335 clocks. (The two-wide FMA has the same
+            // rate, and as a 64-bit operation on the accumulators it takes 254
+            // registers where this takes 184; under the limit here it ran at
+            // ~800 clocks, in register moves.)
+            constexpr int NCH = CW / 16;
+            uint32_t r[2][16];
+            auto block_addr = [&]() { return tmem_base + t_off + buf * NSUB * Cfg::TMEM_STRIDE; };
+            auto wait_block = [&]() {
+                if (!wait_warp(&tfull_bar[buf * NSUB + s], buf_phase, p, s_abort)) return false;
+                tc_fence_after();
+                return true;
+            };
+            const int kb1 = min(4 * c.kg1, p.kb);
             load_group(c.kg0);
+            if (!wait_block()) break;
+            tmem_ld_32x32b_x16(block_addr(), r[0]);
             for (int kg = c.kg0; kg < c.kg1 && !aborted; ++kg) {
                 float s0[4];
                 [[maybe_unused]] float s1[4];
@@ -527,47 +533,50 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 if (kg + 1 < c.kg1) load_group(kg + 1);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if (4 * kg + i >= p.kb) break;
+                    if (4 * kg + i >= kb1) break;
                     const int b = buf * NSUB + s;
-                    if (!wait_warp(&tfull_bar[b], buf_phase, p, s_abort)) { aborted = true; break; }
-                    tc_fence_after();
-                    const uint32_t taddr = tmem_base + t_off + buf * NSUB * Cfg::TMEM_STRIDE;
-                    const uint64_t f0 = pack_f32x2(__float_as_uint(s0[i]), __float_as_uint(s0[i]));
-                    [[maybe_unused]] uint64_t f1 = 0;
-                    if constexpr (kTwoBlocks) f1 = pack_f32x2(__float_as_uint(s1[i]), __float_as_uint(s1[i]));
-                    // 16 columns at a time, the next 16 in flight
-                    uint32_t r[2][16];
-                    tmem_ld_32x32b_x16(taddr, r[0]);
+                    const uint32_t taddr = block_addr();
 #pragma unroll
-                    for (int h = 0; h < CW; h += 16) {
-                        uint32_t (&v)[16] = r[(h / 16) & 1];
+                    for (int ch = 0; ch < NCH; ++ch) {
+                        const int h = 16 * ch;
+                        uint32_t (&v)[16] = r[(i * NCH + ch) & 1];
+                        uint32_t (&nxt)[16] = r[(i * NCH + ch + 1) & 1];
                         tc_wait_ld16(v);
-                        if (h + 16 < CW) {
-                            tmem_ld_32x32b_x16(taddr + h + 16, r[(h / 16 + 1) & 1]);
+                        if (ch + 1 < NCH) {
+                            tmem_ld_32x32b_x16(taddr + h + 16, nxt);
                         } else {
-                            // last read of this buffer: hand it back to the MMA warp
+                            // last read of this buffer: hand it back to the MMA
+                            // warp, and start on the next block's
                             tc_fence_before();
                             __syncwarp();
                             if (lane == 0) {
                                 if (CG == 1 || leader) mbar_arrive(&tempty_bar[b]);
                                 else mbar_arrive_cluster(tempty_leader0 + 8u * static_cast<uint32_t>(b));
                             }
+                            if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+                            if (4 * kg + i + 1 < kb1) {
+                                if (!wait_block()) { aborted = true; break; }
+                                tmem_ld_32x32b_x16(block_addr(), nxt);
+                            }
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            const uint64_t x = pack_f32x2(v[j], v[j + 1]);
-                            uint64_t& a = acc[(h + j) / 2];
+                        for (int j = 0; j < 16; j += 4) {
+                            float sb[4] = {1.f, 1.f, 1.f, 1.f};
                             if constexpr (ROWB) {
-                                const uint64_t sb = *reinterpret_cast<const uint64_t*>(sfb_cols + i * BN + h + j);
-                                a = fma_f32x2(mul_f32x2(x, sb), f0, a);
-                            } else if constexpr (kTwoBlocks) {
-                                a = fma_f32x2(x, h < first_cols ? f0 : f1, a);
-                            } else {
-                                a = fma_f32x2(x, f0, a);
+                                const float4 f = *reinterpret_cast<const float4*>(sfb_cols + i * BN + h + j);
+                                sb[0] = f.x; sb[1] = f.y; sb[2] = f.z; sb[3] = f.w;
+                            }
+                            float f = s0[i];
+                            if constexpr (kTwoBlocks) f = h < first_cols ? s0[i] : s1[i];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                float x = __uint_as_float(v[j + e]);
+                                if constexpr (ROWB) x *= sb[e];
+                                acc[h + j + e] = fmaf(x, f, acc[h + j + e]);
                             }
                         }
                     }
-                    if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+                    if (aborted) break;
                 }
             }
             if (aborted) break;
@@ -578,12 +587,8 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                     float* part = reinterpret_cast<float*>(smem_a) + (32 * q + lane) * Cfg::PART_ROW + col_in_tile;
                     if (mloc < p.rows) {
 #pragma unroll
-                        for (int i = 0; i < CW / 2; i += 2) {
-                            float f[4];
-                            unpack_f32x2(acc[i], f[0], f[1]);
-                            unpack_f32x2(acc[i + 1], f[2], f[3]);
-                            *reinterpret_cast<float4*>(part + 2 * i) = make_float4(f[0], f[1], f[2], f[3]);
-                        }
+                        for (int i = 0; i < CW; i += 4)
+                            *reinterpret_cast<float4*>(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
                     }
                     continue;
                 }
@@ -605,6 +610,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             to.rows = __ballot_sync(0xffffffffu, valid);
             if (to.rows != 0) store_rows<CW, Cfg::STG_ROW>(p, acc, to, col0, stg, static_cast<int>(lane));
         }
+        tc_wait_ld();  // a read in flight when a wait gave up
     }
 
     tc_fence_before();
