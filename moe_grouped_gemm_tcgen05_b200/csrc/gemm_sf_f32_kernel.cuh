@@ -111,6 +111,29 @@ __device__ __forceinline__ void registers_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Two FMAs in one instruction: a += x * f. It takes the FMA pipe for two cycles
+// and the issue slot for one. That matters more than its own speed: with
+// one-wide FMAs the epilogue's warps fill the issue slots of their scheduler, and
+// the MMA warp that shares it issues a block's MMAs in ~890 clocks instead of
+// 512 (microbenchmark, N = 256).
+__device__ __forceinline__ void fma2(float& a0, float& a1, float x0, float x1, float f0, float f1) {
+    asm("{\n\t.reg .b64 a, x, f;\n\t"
+        "mov.b64 a, {%0, %1};\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 f, {%4, %5};\n\t"
+        "fma.rn.f32x2 a, x, f, a;\n\t"
+        "mov.b64 {%0, %1}, a;\n\t}"
+        : "+f"(a0), "+f"(a1) : "f"(x0), "f"(x1), "f"(f0), "f"(f1));
+}
+__device__ __forceinline__ void mul2(float& y0, float& y1, float x0, float x1, float f0, float f1) {
+    asm("{\n\t.reg .b64 y, x, f;\n\t"
+        "mov.b64 x, {%2, %3};\n\t"
+        "mov.b64 f, {%4, %5};\n\t"
+        "mul.rn.f32x2 y, x, f;\n\t"
+        "mov.b64 {%0, %1}, y;\n\t}"
+        : "=f"(y0), "=f"(y1) : "f"(x0), "f"(x1), "f"(f0), "f"(f1));
+}
+
 __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     float4 v;
     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
@@ -492,11 +515,8 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             };
             // The block products, 16 columns at a time in two sets of registers: a
             // chunk's read is issued before the chunk before it is added, across
-            // blocks too, so that the reads pass under the FMAs. 8 warps read and
-            // add 128 columns each in ~335 clocks. (The two-wide FMA has the same
-            // rate, and as a 64-bit operation on the accumulators it takes 254
-            // registers where this takes 184; under the limit here it ran at
-            // ~800 clocks, in register moves.)
+            // blocks too, so that the reads pass under the FMAs. Eight warps read
+            // and add 128 columns each in ~285 clocks (microbenchmark).
             constexpr int NCH = CW / 16;
             uint32_t r[2][16];
             auto block_addr = [&]() { return tmem_base + t_off + buf * NSUB * Cfg::TMEM_STRIDE; };
@@ -569,10 +589,10 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                             float f = s0[i];
                             if constexpr (kTwoBlocks) f = h < first_cols ? s0[i] : s1[i];
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                float x = __uint_as_float(v[j + e]);
-                                if constexpr (ROWB) x *= sb[e];
-                                acc[h + j + e] = fmaf(x, f, acc[h + j + e]);
+                            for (int e = 0; e < 4; e += 2) {
+                                float x0 = __uint_as_float(v[j + e]), x1 = __uint_as_float(v[j + e + 1]);
+                                if constexpr (ROWB) mul2(x0, x1, x0, x1, sb[e], sb[e + 1]);
+                                fma2(acc[h + j + e], acc[h + j + e + 1], x0, x1, f, f);
                             }
                         }
                     }
