@@ -22,20 +22,17 @@ struct Entry {
     void* fn;
 };
 
-template <int BN, int KIND, int CG, int NSUB, bool ROWB>
+template <int KIND, int CG, bool ROWB>
 Entry entry() {
-    using Cfg = dg::SfF32Config<BN, CG, NSUB, dg::sched_ints<KIND>(), ROWB>;
-    return {BN, KIND, CG, ROWB, Cfg::SUB_B_ROWS, dg::SF_F32_THREADS, Cfg::SMEM_BYTES, Cfg::STAGES,
-            reinterpret_cast<void*>(&dg::fp8_gemm_sf_f32_kernel<BN, KIND, CG, NSUB, ROWB>)};
+    using Cfg = dg::SfF32Config<CG, dg::sched_ints<KIND>(), ROWB>;
+    return {Cfg::BN, KIND, CG, ROWB, Cfg::B_ROWS, dg::SF_F32_THREADS, Cfg::SMEM_BYTES, Cfg::STAGES,
+            reinterpret_cast<void*>(&dg::fp8_gemm_sf_f32_kernel<KIND, CG, ROWB>)};
 }
 
 const Entry kEntries[] = {
-    entry<128, dg::kDense, 1, 1, false>(),      entry<192, dg::kDense, 2, 1, false>(),
-    entry<224, dg::kDense, 2, 1, false>(),     entry<256, dg::kDense, 2, 1, false>(),
-    entry<128, dg::kDense, 1, 1, true>(),       entry<256, dg::kDense, 2, 1, true>(),
-    entry<128, dg::kContiguous, 1, 1, false>(), entry<224, dg::kContiguous, 2, 1, false>(),
-    entry<256, dg::kContiguous, 2, 1, false>(),
-    entry<128, dg::kMasked, 1, 1, false>(),
+    entry<dg::kDense, 1, false>(),      entry<dg::kDense, 2, false>(),      entry<dg::kDense, 1, true>(),
+    entry<dg::kDense, 2, true>(),       entry<dg::kContiguous, 1, false>(), entry<dg::kContiguous, 2, false>(),
+    entry<dg::kMasked, 1, false>(),
 };
 constexpr int kNumEntries = sizeof(kEntries) / sizeof(kEntries[0]);
 

@@ -19,8 +19,7 @@
 // CTA = 12 warps (three warpgroups), one CTA per SM, persistent:
 //   warp 0      TMA producer (128-byte swizzle, STAGES-deep ring)
 //   warp 1      TMEM allocation and MMA issue
-//   warps 2, 3  idle; they complete the first warpgroup, whose registers go to
-//               the epilogue (56 + 2 x 224 of the launch's 3 x 168 per lane)
+//   warp 3      scales: (72 + 2 x 216 of the launch's 3 x 168 per lane)
 //   warps 4..   epilogue. Warp w reads TMEM lanes 32 (w % 4) .. + 31 (a row per
 //               lane) and owns half of the tile's columns, CW = BN / 2, whose
 //               accumulators stay in its registers over the whole K loop. 32
@@ -80,17 +79,27 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t m, uint32_t n) {
          | ((m >> 4) << 24);     // M >> 4
 }
 
-// Wait for the TMEM loads into r; naming the registers keeps their uses behind the wait.
-__device__ __forceinline__ void tc_wait_ld16(uint32_t (&r)[16]) {
-    asm volatile("tcgen05.wait::ld.sync.aligned;"
-                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                   "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
-                   "+r"(r[15])
-                 :: "memory");
+// Columns of TMEM (32 lanes x N, N a multiple of 16) into registers, and the
+// wait for them; naming the registers keeps their uses behind the wait.
+template <int N>
+__device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[N]) {
+    static_assert(N % 16 == 0, "16 columns at a time");
+#pragma unroll
+    for (int h = 0; h + 32 <= N; h += 32) tmem_ld_32x32b_x32(taddr + h, r + h);
+    if constexpr (N % 32 != 0) tmem_ld_32x32b_x16(taddr + N - 16, r + N - 16);
+}
+template <int N>
+__device__ __forceinline__ void tmem_read_done(uint32_t (&r)[N]) {
+    tc_wait_ld();
+#pragma unroll
+    for (int h = 0; h < N; h += 16)
+        asm volatile("" : "+r"(r[h]), "+r"(r[h + 1]), "+r"(r[h + 2]), "+r"(r[h + 3]), "+r"(r[h + 4]), "+r"(r[h + 5]),
+                          "+r"(r[h + 6]), "+r"(r[h + 7]), "+r"(r[h + 8]), "+r"(r[h + 9]), "+r"(r[h + 10]),
+                          "+r"(r[h + 11]), "+r"(r[h + 12]), "+r"(r[h + 13]), "+r"(r[h + 14]), "+r"(r[h + 15]));
 }
 
 // Scale loads that stay where they are written: left to itself the compiler moves
-// them down to their use, four K-blocks later, and the warp waits for L2 there.
+// them down to their use, a group of blocks later.
 __device__ __forceinline__ float ld_scale(const float* p) {
     float v;
     asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
@@ -99,6 +108,35 @@ __device__ __forceinline__ float ld_scale(const float* p) {
 __device__ __forceinline__ void ld_scale4(const float* p, float (&v)[4]) {
     asm volatile("ld.global.nc.v4.f32 {%0, %1, %2, %3}, [%4];"
                  : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]) : "l"(p));
+}
+
+__device__ __forceinline__ void mbar_arrive_addr(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool mbar_try_wait_addr(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+template <int CG>
+__device__ __forceinline__ void tc_commit_addr(uint32_t bar) {
+    if constexpr (CG == 1)
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;"
+            ::"r"(bar), "h"(static_cast<uint16_t>(0x3)) : "memory");
+}
+
+// wait_warp whose first probe is all that a ready barrier costs: the epilogue and
+// the MMA warps wait twice per K-block.
+__device__ __forceinline__ bool wait_block(uint64_t* bar, uint32_t parity, const GemmParams& p, volatile int* s_abort) {
+    if (__builtin_expect(__all_sync(0xffffffffu, mbar_try_wait(bar, parity)) != 0, 1)) return true;
+    return wait_warp(bar, parity, p, s_abort);
 }
 
 // Registers of the calling warpgroup from here on (per thread).
@@ -141,44 +179,43 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t addr) {
     return v;
 }
 
-// ROWB: B is scaled per row (sfb_gran_n = 1).
 constexpr int SF_F32_THREADS = 384;
+constexpr int SF_F32_ISSUERS = 2;                     // warps that issue MMAs (warps 1 and 2)
 constexpr int SF_F32_EPI_WARP0 = 4;                   // first epilogue warp
-constexpr int SF_F32_LAUNCH_REGS = 168, SF_F32_EPI_REGS = 224, SF_F32_OTHER_REGS = 56;
+constexpr int SF_F32_BN = 128;                        // columns of a tile
+constexpr int SF_F32_LAUNCH_REGS = 168, SF_F32_EPI_REGS = 208, SF_F32_OTHER_REGS = 88;
 static_assert(SF_F32_OTHER_REGS + 2 * SF_F32_EPI_REGS <= 3 * SF_F32_LAUNCH_REGS, "registers of the launch");
 
-template <int BN, int CG, int NSUB, int SCHED_INTS, bool ROWB>
+// ROWB: B is scaled per row (sfb_gran_n = 1).
+template <int CG, int SCHED_INTS, bool ROWB>
 struct SfF32Config {
+    static constexpr int BN = SF_F32_BN;
     static constexpr int EW = 8;                      // epilogue warps
-    static constexpr int GROUPS = EW / 4;             // column groups of epilogue warps
-    static constexpr int CW = BN / GROUPS;            // columns of an epilogue warp
-    static constexpr int SUB = BN / NSUB;             // columns of a sub-tile (one MMA's N)
+    static constexpr int CW = BN / 2;                 // columns of an epilogue warp
     static constexpr int B_ROWS = BN / CG;            // rows of B in this CTA's shared memory
-    static constexpr int SUB_B_ROWS = SUB / CG;
-    static_assert(BN % GROUPS == 0 && CW % 16 == 0 && SUB % CW == 0, "columns of an epilogue warp");
-    static_assert(SUB % 16 == 0 && SUB <= 256 && SUB_B_ROWS % 8 == 0, "N of an MMA");
-    static_assert(!ROWB || BN % 128 == 0, "per-row scales: one column per lane and K-block");
     static constexpr int A_BYTES = BM * BK;
     static constexpr int B_BYTES = B_ROWS * BK;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
-    // columns between TMEM buffers; all 512 columns are used
-    static constexpr int TMEM_STRIDE = SUB > 128 ? 256 : (SUB > 64 ? 128 : 64);
-    static constexpr int NBUF = 512 / (NSUB * TMEM_STRIDE);
-    static_assert(NBUF >= 2, "the MMAs of a block run while the last one is read back");
+    static constexpr int NBUF = 512 / BN;             // TMEM buffers of a block product
     // output staging: 32 rows of 64 bytes per epilogue warp, rows 80 bytes apart (no bank conflicts)
     static constexpr int STG_ROW = 80;
     static constexpr int STG_BYTES = EW * 32 * STG_ROW;
-    static constexpr int SFB_BYTES = ROWB ? 2 * 4 * BN * 4 : 0;  // two groups of four K-blocks' column scales
+    // scales of four K-blocks per slot: [4][128 rows] (times B's, when that is one
+    // per 128 columns), and with ROWB [4][BN columns]
+    static constexpr int SF_SLOTS = 2;
+    static constexpr int SF_SLOT_FLOATS = 4 * BM + (ROWB ? 4 * BN : 0);
+    static constexpr int SF_BYTES = SF_SLOTS * SF_SLOT_FLOATS * 4;
     static constexpr int SCHED_BYTES = SCHED_INTS * 4;
-    static constexpr int FIXED_BYTES = 1024 /*align slack*/ + STG_BYTES + SFB_BYTES + 512 /*barriers*/ + SCHED_BYTES;
+    static constexpr int FIXED_BYTES = 1024 /*align slack*/ + STG_BYTES + SF_BYTES + 512 /*barriers*/ + SCHED_BYTES;
     static constexpr int STAGES_FIT = (SMEM_LIMIT - FIXED_BYTES) / STAGE_BYTES;
     static constexpr int STAGES = STAGES_FIT > 8 ? 8 : STAGES_FIT;
-    static_assert(STAGES >= 3, "pipeline too shallow");
+    static_assert(STAGES >= NBUF, "a stage's barrier completes again only after its product's buffer was handed back");
     static constexpr int SMEM_BYTES = FIXED_BYTES + STAGES * STAGE_BYTES;
-    static constexpr uint32_t IDESC = idesc_e4m3_f32(BM * CG, SUB);
+    static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory of a CTA");
+    static constexpr uint32_t IDESC = idesc_e4m3_f32(BM * CG, BN);
     // split-K: a partial tile of fp32 rows, four floats of padding per row
     static constexpr int PART_ROW = BN + 4;
-    static_assert(BM * PART_ROW * 4 <= STAGES * STAGE_BYTES || CG == 2, "the partial tile fits the idle ring");
+    static_assert(BM * PART_ROW * 4 <= STAGES * STAGE_BYTES, "the partial tile fits the idle ring");
 };
 
 // The 128-row share of D that an epilogue warp writes: 32 rows from `row0` of
@@ -193,7 +230,7 @@ struct StoreRows {
 // lanes take the 64 bytes of a row. (Row-wise 16-byte stores straight from the
 // registers touch 32 rows per instruction and slow the operand loads.)
 template <int CW, int STG_ROW>
-__device__ __forceinline__ void store_rows(const GemmParams& p, const float (&acc)[CW], const StoreRows& to,
+__device__ __forceinline__ void store_rows(const GemmParams& p, const float* acc, const StoreRows& to,
                                            int col0, uint8_t* stg, int lane) {
     const int sub = lane >> 2, piece = lane & 3;
     if (p.c == nullptr && !p.out_f32) {
@@ -276,15 +313,15 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const float (&ac
     }
 }
 
-template <int BN, int KIND, int CG, int NSUB, bool ROWB>
+template <int KIND, int CG, bool ROWB>
 __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(const __grid_constant__ SfF32Params p) {
     static_assert(CG == 1 || KIND != kMasked, "CTA pairs are built for the dense and contiguous forms");
     static_assert(!ROWB || KIND == kDense, "per-row scales of B: dense form");
-    using Cfg = SfF32Config<BN, CG, NSUB, sched_ints<KIND>(), ROWB>;
-    constexpr int STAGES = Cfg::STAGES;
-    constexpr int NBUF = Cfg::NBUF;
+    using Cfg = SfF32Config<CG, sched_ints<KIND>(), ROWB>;
+    constexpr int BN = Cfg::BN;
     constexpr int CW = Cfg::CW;
-    constexpr int BUFS = NBUF * NSUB;
+    constexpr int NBUF = Cfg::NBUF;
+    constexpr int STAGES = Cfg::STAGES;
     constexpr bool kCanSplit = KIND == kDense && CG == 1;
 
     extern __shared__ uint8_t smem_raw[];
@@ -292,15 +329,15 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
     uint8_t* smem_a = smem;
     uint8_t* smem_b = smem_a + STAGES * Cfg::A_BYTES;
     uint8_t* smem_stg = smem_b + STAGES * Cfg::B_BYTES;
-    float* smem_sfb = reinterpret_cast<float*>(smem_stg + Cfg::STG_BYTES);    // ROWB: [2][4][BN]
-    uint64_t* bars = reinterpret_cast<uint64_t*>(smem_stg + Cfg::STG_BYTES + Cfg::SFB_BYTES);
+    float* smem_sf = reinterpret_cast<float*>(smem_stg + Cfg::STG_BYTES);
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem_stg + Cfg::STG_BYTES + Cfg::SF_BYTES);
     uint64_t* full_bar = bars;                   // A/B bytes landed (the leader's counts both CTAs)
-    uint64_t* empty_bar = full_bar + STAGES;     // MMAs reading the stage finished
-    uint64_t* tfull_bar = empty_bar + STAGES;    // [buffer][sub-tile]: block product ready
-    uint64_t* tempty_bar = tfull_bar + BUFS;     // [buffer][sub-tile]: read back
-    uint64_t* sfb_bar = tempty_bar + BUFS;       // ROWB: a column group's scales are in shared memory
-    uint64_t* drain_bar = sfb_bar + Cfg::GROUPS; // all MMAs issued for this CTA finished
-    static_assert((2 * STAGES + 2 * BUFS + Cfg::GROUPS + 1) * 8 + 16 <= 512, "barrier space");
+    uint64_t* done_bar = full_bar + STAGES;      // block product ready; its stage is read
+    uint64_t* tempty_bar = done_bar + STAGES;    // TMEM buffer read back
+    uint64_t* sfull_bar = tempty_bar + NBUF;     // scales of four K-blocks are in shared memory
+    uint64_t* sempty_bar = sfull_bar + Cfg::SF_SLOTS;   // ... and used by every epilogue warp
+    uint64_t* drain_bar = sempty_bar + Cfg::SF_SLOTS;         // all MMAs issued for this CTA finished
+    static_assert((2 * STAGES + NBUF + 2 * Cfg::SF_SLOTS + 1) * 8 + 16 <= 512, "barrier space");
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain_bar + 1);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     int* s_prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
@@ -317,14 +354,14 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full_bar[s], 1);
-            mbar_init(&empty_bar[s], 1);
+            mbar_init(&done_bar[s], 1);
         }
-        for (int i = 0; i < BUFS; ++i) {
-            mbar_init(&tfull_bar[i], 1);
-            mbar_init(&tempty_bar[i], Cfg::EW / NSUB * CG);
+        for (int i = 0; i < NBUF; ++i) mbar_init(&tempty_bar[i], Cfg::EW * CG);
+        for (int i = 0; i < Cfg::SF_SLOTS; ++i) {
+            mbar_init(&sfull_bar[i], 1);
+            mbar_init(&sempty_bar[i], Cfg::EW);
         }
-        for (int i = 0; i < Cfg::GROUPS; ++i) mbar_init(&sfb_bar[i], 4);
-        mbar_init(drain_bar, 1);
+        mbar_init(drain_bar, SF_F32_ISSUERS);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -360,11 +397,11 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
         for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
              t += units) {
             const int a_row = cur.m_blk * BM * CG + my_rows;
-            const int b_row = cur.n_blk * BN + Cfg::SUB_B_ROWS * static_cast<int>(rank);
+            const int b_row = cur.n_blk * BN + Cfg::B_ROWS * static_cast<int>(rank);
             const int g = max(cur.g, 0);
             const int kb1 = min(4 * cur.kg1, p.kb);
             for (int kb = 4 * cur.kg0; kb < kb1; ++kb) {
-                if (issued >= STAGES && !wait_warp(&empty_bar[stage], phase ^ 1u, p, s_abort)) { aborted = true; break; }
+                if (issued >= STAGES && !wait_warp(&done_bar[stage], phase ^ 1u, p, s_abort)) { aborted = true; break; }
                 // (the failure-path hook withholds CTA 0's first load)
                 if (elect_one() && !(p.test_mode == 1 && blockIdx.x == 0 && issued == 0)) {
                     uint8_t* a_dst = smem_a + stage * Cfg::A_BYTES;
@@ -379,19 +416,13 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                         if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
                         tma_load_2d_pair(a_dst, &p.tma_a, full_leader0 + 8u * static_cast<uint32_t>(stage), kx, a_row);
                     }
-#pragma unroll
-                    for (int s = 0; s < NSUB; ++s) {
-                        // sub-tile s: this CTA's SUB / CG rows of it
-                        uint8_t* dst = b_dst + s * Cfg::SUB_B_ROWS * BK;
-                        const int row = b_row + s * Cfg::SUB;
-                        if constexpr (CG == 1) {
-                            if constexpr (KIND == kDense) tma_load_2d(dst, &p.tma_b, &full_bar[stage], kx, row);
-                            else tma_load_3d(dst, &p.tma_b, &full_bar[stage], kx, row, g);
-                        } else {
-                            const uint32_t fb = full_leader0 + 8u * static_cast<uint32_t>(stage);
-                            if constexpr (KIND == kDense) tma_load_2d_pair(dst, &p.tma_b, fb, kx, row);
-                            else tma_load_3d_pair(dst, &p.tma_b, fb, kx, row, g);
-                        }
+                    if constexpr (CG == 1) {
+                        if constexpr (KIND == kDense) tma_load_2d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row);
+                        else tma_load_3d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row, g);
+                    } else {
+                        const uint32_t fb = full_leader0 + 8u * static_cast<uint32_t>(stage);
+                        if constexpr (KIND == kDense) tma_load_2d_pair(b_dst, &p.tma_b, fb, kx, b_row);
+                        else tma_load_3d_pair(b_dst, &p.tma_b, fb, kx, b_row, g);
                     }
                 }
                 __syncwarp();
@@ -412,206 +443,199 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 sleep_ns(p.wait_limit_ns / 16);
             }
         }
-    } else if (warp == 1) {
-        // ---------------------------------------------------------- MMA issuer --
+    } else if (warp <= SF_F32_ISSUERS) {
+        // --------------------------------------------------------- MMA issuers --
+        // Block products are dealt out in turn: two waits, four MMAs and two
+        // commits take a lone warp ~450 clocks next to the epilogue's warps,
+        // longer than the MMAs run.
         if (CG == 1 || leader) {
-            int stage = 0, gcur = 0, buf = 0;
-            uint32_t phase = 0, buf_phase = 0;
+            const uint32_t mine = warp - 1;
+            const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem_a));
+            const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem_b));
+            const uint32_t full0 = smem_u32(full_bar), tempty0 = smem_u32(tempty_bar), done0 = smem_u32(done_bar);
+            int gcur = 0;
+            uint32_t item0 = 0;   // block products before this tile
+            uint32_t stage = mine, par = 0;   // of this warp's next product
             Tile c;
             bool aborted = false;
             for (int t = unit; !aborted && next_tile<KIND, CG == 2, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
                  t += units) {
-                const int kb1 = min(4 * c.kg1, p.kb);
-                for (int kb = 4 * c.kg0; kb < kb1 && !aborted; ++kb) {
-                    if (!wait_warp(&full_bar[stage], phase, p, s_abort)) { aborted = true; break; }
-                    const uint64_t adesc = smem_desc_sw128(smem_u32(smem_a + stage * Cfg::A_BYTES));
-                    const uint64_t bdesc = smem_desc_sw128(smem_u32(smem_b + stage * Cfg::B_BYTES));
-#pragma unroll
-                    for (int s = 0; s < NSUB; ++s) {
-                        const int b = buf * NSUB + s;
-                        if (!wait_warp(&tempty_bar[b], buf_phase ^ 1u, p, s_abort)) { aborted = true; break; }
-                        tc_fence_after();  // the epilogue's reads of this buffer precede the MMAs below
-                        if (elect_one()) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const uint64_t koff = static_cast<uint64_t>((k * 32) >> 4);
-                                const uint64_t soff = static_cast<uint64_t>((s * Cfg::SUB_B_ROWS * BK) >> 4);
-                                tc_mma_f8<CG>(tmem_base + b * Cfg::TMEM_STRIDE, adesc + koff, bdesc + soff + koff,
-                                              Cfg::IDESC, k > 0 ? 1u : 0u);
-                            }
-                            tc_commit<CG>(&tfull_bar[b]);
-                            if (s == NSUB - 1) tc_commit<CG>(&empty_bar[stage]);
-                        }
-                        __syncwarp();
+                const uint32_t n = static_cast<uint32_t>(min(4 * c.kg1, p.kb) - 4 * c.kg0);
+                // the products whose number has this warp's parity
+                for (uint32_t it = item0 + ((item0 ^ mine) & 1u); it < item0 + n; it += 2) {
+                    // operands landed, and the buffer's last product read back: both probes at once
+                    const uint32_t buf = it % NBUF, buf_par = ((it / NBUF) & 1u) ^ 1u;
+                    const bool ready = mbar_try_wait_addr(full0 + 8 * stage, par) & mbar_try_wait_addr(tempty0 + 8 * buf, buf_par);
+                    if (!__all_sync(0xffffffffu, ready) && !(wait_warp(&full_bar[stage], par, p, s_abort) &&
+                                                            wait_warp(&tempty_bar[buf], buf_par, p, s_abort))) {
+                        aborted = true;
+                        break;
                     }
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-                    if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
+                    tc_fence_after();  // the epilogue's reads of this buffer precede the MMAs below
+                    const uint64_t adesc = adesc0 + stage * (Cfg::A_BYTES >> 4), bdesc = bdesc0 + stage * (Cfg::B_BYTES >> 4);
+                    if (elect_one()) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            tc_mma_f8<CG>(tmem_base + buf * BN, adesc + 2 * k, bdesc + 2 * k, Cfg::IDESC, k > 0 ? 1u : 0u);
+                        tc_commit_addr<CG>(done0 + 8 * stage);
+                    }
+                    __syncwarp();
+                    stage += 2;
+                    if (stage >= STAGES) { stage -= STAGES; par ^= 1u; }
                 }
+                item0 += n;
             }
             if (elect_one()) tc_commit<CG>(drain_bar);
             __syncwarp();
         }
         wait_quiet(drain_bar, 0, p.wait_limit_ns);
+    } else {
+        // ------------------------------------------------------ scale producer --
+        // Gathers the scales of four K-blocks of every row (lane l: rows l, l + 32,
+        // ...) into shared memory, the next four K-blocks' loads in flight. (Read
+        // by the epilogue's warps from global memory, even several blocks ahead,
+        // the scales held them up for ~300 clocks a block.)
+        float a[2][4][4], b[2][ROWB ? 4 : 1][4];   // [set][row][K-block]
+        auto load4 = [&](const float* row, int kb0, bool vec, float (&v)[4]) {
+            if (vec) {
+                ld_scale4(row + kb0, v);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = ld_scale(row + min(kb0 + i, p.kb - 1));
+            }
+        };
+        uint32_t stored = 0;
+        auto store = [&](int set) {
+            const uint32_t slot = stored % Cfg::SF_SLOTS;
+            if (!wait_block(&sempty_bar[slot], ((stored / Cfg::SF_SLOTS) & 1u) ^ 1u, p, s_abort)) return false;
+            float* dst = smem_sf + slot * Cfg::SF_SLOT_FLOATS + lane;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dst[i * BM + 32 * j] = ROWB ? a[set][j][i] : a[set][j][i] * b[set][0][i];
+                    if constexpr (ROWB) dst[4 * BM + i * BN + 32 * j] = b[set][j][i];
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfull_bar[slot]);
+            ++stored;
+            return true;
+        };
+        int gcur = 0;
+        Tile c;
+        bool aborted = false;
+        for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+             t += units) {
+            // rows and columns clamped into the operands (those past them are never stored)
+            const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
+            const int row0 = c.m_blk * BM * CG + my_rows + static_cast<int>(lane);
+            const float* sfb = p.sfb32 + static_cast<size_t>(KIND == kDense ? 0 : max(c.g, 0)) * p.nb_sf * p.kb;
+            auto load = [&](int set, int kg) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    load4(p.sfa32 + (a_base + min(row0 + 32 * j, p.rows - 1)) * p.kb, 4 * kg, p.sfa_vec4 != 0, a[set][j]);
+#pragma unroll
+                for (int j = 0; j < (ROWB ? 4 : 1); ++j) {
+                    const int row = ROWB ? min(c.n_blk * BN + 32 * j + static_cast<int>(lane), p.n - 1) : c.n_blk;
+                    load4(sfb + static_cast<size_t>(row) * p.kb, 4 * kg, p.sfb_vec4 != 0, b[set][j]);
+                }
+            };
+            load(0, c.kg0);
+            for (int kg = c.kg0; kg < c.kg1; kg += 2) {
+                if (kg + 1 < c.kg1) load(1, kg + 1);
+                if (!store(0)) { aborted = true; break; }
+                if (kg + 1 >= c.kg1) break;
+                if (kg + 2 < c.kg1) load(0, kg + 2);
+                if (!store(1)) { aborted = true; break; }
+            }
+        }
     }
     } else {
         registers_inc<SF_F32_EPI_REGS>();
         // ------------------------------------------------------------ epilogue --
         const int q = static_cast<int>(warp & 3);              // TMEM lanes 32q .. 32q + 31
-        const int grp = static_cast<int>(warp - SF_F32_EPI_WARP0) / 4;  // column group
-        const int col_in_tile = grp * CW;
-        const int s = col_in_tile / Cfg::SUB;                  // sub-tile
-        const uint32_t t_off = (static_cast<uint32_t>(32 * q) << 16) + s * Cfg::TMEM_STRIDE + (col_in_tile - s * Cfg::SUB);
+        const int grp = static_cast<int>(warp - SF_F32_EPI_WARP0) / 4;  // columns CW grp ...
+        const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + grp * CW;
         uint8_t* stg = smem_stg + (warp - SF_F32_EPI_WARP0) * 32 * Cfg::STG_ROW;
-        [[maybe_unused]] uint32_t tempty_leader0 = 0;
-        if constexpr (CG == 2) tempty_leader0 = mapa_shared(smem_u32(&tempty_bar[0]), 0);
-        // a warp's columns can lie in two 128-column blocks of B when the tile width is no multiple of 128
-        constexpr bool kTwoBlocks = !ROWB && BN % 128 != 0;
-        int buf = 0, gcur = 0;
-        uint32_t buf_phase = 0;
-        [[maybe_unused]] uint32_t sfb_slot = 0, sfb_phase = 0;
+        const uint32_t done0 = smem_u32(done_bar);
+        const uint32_t tempty0 = CG == 1 ? smem_u32(tempty_bar) : mapa_shared(smem_u32(tempty_bar), 0);
+        int gcur = 0;
+        uint32_t stage = 0, par = 0, buf = 0;
+        uint32_t sf_group = 0;       // groups of four K-blocks before this one
         bool aborted = false;
         Tile c;
         for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
              t += units) {
             const int mloc = c.m_blk * BM * CG + my_rows + 32 * q + static_cast<int>(lane);
-            const int col0 = c.n_blk * BN + col_in_tile;
-            // scale rows, clamped into the operands (rows and columns past them are never stored)
             const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
-            const float* sa = p.sfa32 + (a_base + min(mloc, p.rows - 1)) * p.kb;
-            const float* sbg = p.sfb32 + static_cast<size_t>(KIND == kDense ? 0 : max(c.g, 0)) * p.nb_sf * p.kb;
-            const float* sb0 = sbg + static_cast<size_t>(min(col0 / 128, p.nb_sf - 1)) * p.kb;
-            [[maybe_unused]] const float* sb1 = sbg + static_cast<size_t>(min((col0 + CW - 1) / 128, p.nb_sf - 1)) * p.kb;
-            // columns of this warp before the next 128-column block
-            [[maybe_unused]] const int first_cols = 128 - (col0 & 127);
-
             float acc[CW];
 #pragma unroll
             for (int i = 0; i < CW; ++i) acc[i] = 0.f;
 
-            // scales of four K-blocks, the next four in flight
-            float na[4], nb[4];
-            [[maybe_unused]] float nb1[4];
-            auto load4 = [&](const float* row, int kb0, bool vec, float (&v)[4]) {
-                if (vec) {
-                    ld_scale4(row + kb0, v);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = ld_scale(row + min(kb0 + i, p.kb - 1));
-                }
-            };
-            // ROWB: the four warps of a column group share its CW columns' scales:
-            // warp q fetches CW / 4 of them (lane = column)
-            constexpr int kColLanes = CW / 4;
-            static_assert(!ROWB || kColLanes <= 32, "one column per lane");
-            auto load_group = [&](int kg) {
-                load4(sa, 4 * kg, p.sfa_vec4 != 0, na);
-                if constexpr (ROWB) {
-                    const int col = min(col0 + q * kColLanes + static_cast<int>(lane) % kColLanes, p.n - 1);
-                    load4(sbg + static_cast<size_t>(col) * p.kb, 4 * kg, p.sfb_vec4 != 0, nb);
-                } else {
-                    load4(sb0, 4 * kg, p.sfb_vec4 != 0, nb);
-                    if constexpr (kTwoBlocks) load4(sb1, 4 * kg, p.sfb_vec4 != 0, nb1);
-                }
-            };
-            // The block products, 16 columns at a time in two sets of registers: a
-            // chunk's read is issued before the chunk before it is added, across
-            // blocks too, so that the reads pass under the FMAs. Eight warps read
-            // and add 128 columns each in ~285 clocks (microbenchmark).
-            constexpr int NCH = CW / 16;
-            uint32_t r[2][16];
-            auto block_addr = [&]() { return tmem_base + t_off + buf * NSUB * Cfg::TMEM_STRIDE; };
-            auto wait_block = [&]() {
-                if (!wait_warp(&tfull_bar[buf * NSUB + s], buf_phase, p, s_abort)) return false;
-                tc_fence_after();
-                return true;
-            };
             const int kb1 = min(4 * c.kg1, p.kb);
-            load_group(c.kg0);
-            if (!wait_block()) break;
-            tmem_ld_32x32b_x16(block_addr(), r[0]);
-            for (int kg = c.kg0; kg < c.kg1 && !aborted; ++kg) {
-                float s0[4];
-                [[maybe_unused]] float s1[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    s0[i] = ROWB ? na[i] : na[i] * nb[i];
-                    if constexpr (kTwoBlocks) s1[i] = na[i] * nb1[i];
-                }
-                [[maybe_unused]] const float* sfb_cols = smem_sfb + sfb_slot * 4 * BN + col_in_tile;
-                if constexpr (ROWB) {
-                    float* dst = smem_sfb + sfb_slot * 4 * BN + col_in_tile;
-                    if (static_cast<int>(lane) < kColLanes) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) dst[i * BN + q * kColLanes + lane] = nb[i];
+            for (int kb = 4 * c.kg0; kb < kb1; kb += 4) {
+                const uint32_t slot = sf_group % Cfg::SF_SLOTS;
+                if (!wait_block(&sfull_bar[slot], (sf_group / Cfg::SF_SLOTS) & 1u, p, s_abort)) { aborted = true; break; }
+                const float* sf = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 32 * q + lane;
+                [[maybe_unused]] const float* sfb_cols = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 4 * BM + grp * CW;
+                const int n = min(4, kb1 - kb);
+                // (not unrolled: the loop's code stays in the innermost instruction cache)
+#pragma unroll 1
+                for (int i = 0; i < n; ++i) {
+                    const float f = sf[i * BM];
+                    if (!__all_sync(0xffffffffu, mbar_try_wait_addr(done0 + 8 * stage, par)) &&
+                        !wait_warp(&done_bar[stage], par, p, s_abort)) {
+                        aborted = true;
+                        break;
                     }
+                    tc_fence_after();
+                    // The whole product is read and its buffer handed back before
+                    // anything is added, and nothing is carried to the next block
+                    // but the sums.
+                    uint32_t r[CW];
+                    tmem_read<CW>(t_row + buf * BN, r);
+                    tmem_read_done<CW>(r);
+                    tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&sfb_bar[grp]);
-                    if (!wait_warp(&sfb_bar[grp], sfb_phase, p, s_abort)) { aborted = true; break; }
-                    sfb_phase ^= 1u;
-                    sfb_slot ^= 1u;  // the other slot's readers have all arrived here
-                }
-                if (kg + 1 < c.kg1) load_group(kg + 1);
+                    if (lane == 0) {
+                        if (CG == 1) mbar_arrive_addr(tempty0 + 8 * buf);
+                        else mbar_arrive_cluster(tempty0 + 8 * buf);
+                    }
+                    buf = (buf + 1) % NBUF;
+                    if (++stage == STAGES) { stage = 0; par ^= 1u; }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (4 * kg + i >= kb1) break;
-                    const int b = buf * NSUB + s;
-                    const uint32_t taddr = block_addr();
-#pragma unroll
-                    for (int ch = 0; ch < NCH; ++ch) {
-                        const int h = 16 * ch;
-                        uint32_t (&v)[16] = r[(i * NCH + ch) & 1];
-                        uint32_t (&nxt)[16] = r[(i * NCH + ch + 1) & 1];
-                        tc_wait_ld16(v);
-                        if (ch + 1 < NCH) {
-                            tmem_ld_32x32b_x16(taddr + h + 16, nxt);
-                        } else {
-                            // last read of this buffer: hand it back to the MMA
-                            // warp, and start on the next block's
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if (CG == 1 || leader) mbar_arrive(&tempty_bar[b]);
-                                else mbar_arrive_cluster(tempty_leader0 + 8u * static_cast<uint32_t>(b));
-                            }
-                            if (++buf == NBUF) { buf = 0; buf_phase ^= 1u; }
-                            if (4 * kg + i + 1 < kb1) {
-                                if (!wait_block()) { aborted = true; break; }
-                                tmem_ld_32x32b_x16(block_addr(), nxt);
-                            }
+                    for (int j = 0; j < CW; j += 4) {
+                        float g[4] = {1.f, 1.f, 1.f, 1.f};
+                        if constexpr (ROWB) {
+                            const float4 g4 = *reinterpret_cast<const float4*>(sfb_cols + i * BN + j);
+                            g[0] = g4.x; g[1] = g4.y; g[2] = g4.z; g[3] = g4.w;
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            float sb[4] = {1.f, 1.f, 1.f, 1.f};
-                            if constexpr (ROWB) {
-                                const float4 f = *reinterpret_cast<const float4*>(sfb_cols + i * BN + h + j);
-                                sb[0] = f.x; sb[1] = f.y; sb[2] = f.z; sb[3] = f.w;
-                            }
-                            float f = s0[i];
-                            if constexpr (kTwoBlocks) f = h < first_cols ? s0[i] : s1[i];
-#pragma unroll
-                            for (int e = 0; e < 4; e += 2) {
-                                float x0 = __uint_as_float(v[j + e]), x1 = __uint_as_float(v[j + e + 1]);
-                                if constexpr (ROWB) mul2(x0, x1, x0, x1, sb[e], sb[e + 1]);
-                                fma2(acc[h + j + e], acc[h + j + e + 1], x0, x1, f, f);
-                            }
+                        for (int e = 0; e < 4; e += 2) {
+                            float x0 = __uint_as_float(r[j + e]), x1 = __uint_as_float(r[j + e + 1]);
+                            if constexpr (ROWB) mul2(x0, x1, x0, x1, g[e], g[e + 1]);
+                            fma2(acc[j + e], acc[j + e + 1], x0, x1, f, f);
                         }
                     }
-                    if (aborted) break;
                 }
+                if (aborted) break;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sempty_bar[slot]);
+                ++sf_group;
             }
             if (aborted) break;
-            if constexpr (kCanSplit) {
-                if (split) {
-                    // this K range's partial, for the cluster's sum below (the ring is
-                    // idle: every MMA of the one tile has been read back)
-                    float* part = reinterpret_cast<float*>(smem_a) + (32 * q + lane) * Cfg::PART_ROW + col_in_tile;
-                    if (mloc < p.rows) {
+
+            if (kCanSplit && split) {
+                // this K range's partial, for the cluster's sum below (the ring is
+                // idle: every MMA of the one tile has been read back)
+                float* part = reinterpret_cast<float*>(smem_a) + (32 * q + lane) * Cfg::PART_ROW + grp * CW;
+                if (mloc < p.rows) {
 #pragma unroll
-                        for (int i = 0; i < CW; i += 4)
-                            *reinterpret_cast<float4*>(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
-                    }
-                    continue;
+                    for (int i = 0; i < CW; i += 4)
+                        *reinterpret_cast<float4*>(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
                 }
+                continue;  // one tile per CTA
             }
             bool valid;
             StoreRows to;
@@ -628,9 +652,9 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 if (in_range && id != own) atomicOr(p.status, DEVERR_MIXED_EXPERT_BLOCK);
             }
             to.rows = __ballot_sync(0xffffffffu, valid);
-            if (to.rows != 0) store_rows<CW, Cfg::STG_ROW>(p, acc, to, col0, stg, static_cast<int>(lane));
+            if (to.rows != 0)
+                store_rows<CW, Cfg::STG_ROW>(p, acc, to, c.n_blk * BN + grp * CW, stg, static_cast<int>(lane));
         }
-        tc_wait_ld();  // a read in flight when a wait gave up
     }
 
     tc_fence_before();

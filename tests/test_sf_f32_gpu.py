@@ -71,7 +71,7 @@ def check(d, ref, mag, K):
     assert np.all(err <= 0), f"{int((err > 0).sum())} of {err.size} off, worst by {err.max():.3g}"
 
 
-TILES = [(128, 1), (192, 2), (224, 2), (256, 2)]
+TILES = [(128, 1), (128, 2)]
 SHAPES = [(1, 8, 128), (7, 136, 384), (128, 128, 512), (130, 264, 640), (257, 520, 1152), (300, 1000, 2048)]
 
 
@@ -86,7 +86,7 @@ def test_dense_every_tile(M, N, K, tile):
     check(d, *om.fp8_gemm_nt_sf_f32(*ops), K)
 
 
-@pytest.mark.parametrize("tile", [(128, 1), (256, 2)])
+@pytest.mark.parametrize("tile", [(128, 1), (128, 2)])
 @pytest.mark.parametrize("M,N,K", SHAPES)
 def test_dense_scales_per_row_of_b(M, N, K, tile):
     ops = operands(M, N, K, gran=1, seed=M + N + 1)
@@ -182,7 +182,7 @@ def test_what_is_not_finite_stays_in_its_row():
 
 def test_guard_bands():
     """D between sentinel rows in one buffer: nothing outside it is written."""
-    for M, N, K, tile in ((130, 264, 256, (128, 1)), (130, 264, 256, (256, 2)), (300, 136, 256, (224, 2)),
+    for M, N, K, tile in ((130, 264, 256, (128, 1)), (130, 264, 256, (128, 2)), (300, 136, 256, (128, 2)),
                           (1, 8, 512, (128, 1))):
         for dtype in (torch.bfloat16, torch.float32):
             dg.set_block_n(tile[0])
@@ -197,7 +197,7 @@ def test_guard_bands():
 
 # ------------------------------------------------------------ grouped forms ----
 
-@pytest.mark.parametrize("tile", [(0, 0), (128, 1), (224, 2), (256, 2)])
+@pytest.mark.parametrize("tile", [(0, 0), (128, 1), (128, 2)])
 @pytest.mark.parametrize("rows,N,K", [([130, 0, 1, 300], 264, 640), ([5], 136, 128), ([128, 128, 256], 512, 1024)])
 def test_contiguous(rows, N, K, tile):
     G = len(rows)
@@ -270,7 +270,7 @@ def test_masked_replay_with_other_counts():
 
 # --------------------------------------------- captured, streams, failure path ----
 
-@pytest.mark.parametrize("M,tile,gran", [(300, (224, 2), 128), (300, (256, 2), 1), (64, (128, 1), 128), (1, (0, 0), 128)])
+@pytest.mark.parametrize("M,tile,gran", [(300, (128, 2), 128), (300, (128, 2), 1), (64, (128, 1), 128), (1, (0, 0), 128)])
 def test_captured_and_replayed(M, tile, gran):
     ops = dev(*operands(M, 400, 2048, gran=gran, seed=M))
     dg.set_block_n(tile[0])
