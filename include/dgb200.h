@@ -428,7 +428,7 @@ DG_API dg_status quantize_fp8_1x128(const void* x, int x_f32, void* q, int32_t* 
  * Every block is accumulated in fp32 by the tensor core, scaled and added in
  * fp32; D is rounded once. Untouched rows, DG_DEVERR_MIXED_EXPERT_BLOCK,
  * limits, errors, bounded waits and capture safety are those of the calls
- * named. quantize_fp8_1x128_sf_f32 makes A and sfa.
+ * named (and at most 2^30 rows and columns). quantize_fp8_1x128_sf_f32 makes A and sfa.
  * The gradients of the dense product Y = X . W^T are the same call: dX = dY . W
  * takes W's codes and its 128x128 scales transposed as B, and dW = dY^T . X
  * takes both operands transposed and quantised along the tokens (sfb_gran_n =

@@ -14,25 +14,27 @@ using dg::is_aligned;
 using dg::SfF32Params;
 
 struct Entry {
-    int bn, kind, cg;
+    int kind, cg;
     bool rowb;      // B scaled per row
-    int sub_b_rows; // rows of B in one load (the tensor map's box)
+    int epi;        // 1: C and / or an fp32 D
+    int b_rows;     // rows of B in one load (the tensor map's box)
     int threads, smem;
     int stages;
     void* fn;
 };
 
-template <int KIND, int CG, bool ROWB>
+template <int KIND, int CG, bool ROWB, int EPI>
 Entry entry() {
     using Cfg = dg::SfF32Config<CG, dg::sched_ints<KIND>(), ROWB>;
-    return {Cfg::BN, KIND, CG, ROWB, Cfg::B_ROWS, dg::SF_F32_THREADS, Cfg::SMEM_BYTES, Cfg::STAGES,
-            reinterpret_cast<void*>(&dg::fp8_gemm_sf_f32_kernel<KIND, CG, ROWB>)};
+    return {KIND, CG, ROWB, EPI, Cfg::B_ROWS, dg::SF_F32_THREADS, Cfg::SMEM_BYTES, Cfg::STAGES,
+            reinterpret_cast<void*>(&dg::fp8_gemm_sf_f32_kernel<KIND, CG, ROWB, EPI>)};
 }
 
 const Entry kEntries[] = {
-    entry<dg::kDense, 1, false>(),      entry<dg::kDense, 2, false>(),      entry<dg::kDense, 1, true>(),
-    entry<dg::kDense, 2, true>(),       entry<dg::kContiguous, 1, false>(), entry<dg::kContiguous, 2, false>(),
-    entry<dg::kMasked, 1, false>(),
+    entry<dg::kDense, 1, false, 0>(), entry<dg::kDense, 2, false, 0>(), entry<dg::kDense, 1, true, 0>(),
+    entry<dg::kDense, 2, true, 0>(),  entry<dg::kDense, 1, false, 1>(), entry<dg::kDense, 2, false, 1>(),
+    entry<dg::kDense, 1, true, 1>(),  entry<dg::kDense, 2, true, 1>(),  entry<dg::kContiguous, 1, false, 0>(),
+    entry<dg::kMasked, 1, false, 0>(),
 };
 constexpr int kNumEntries = sizeof(kEntries) / sizeof(kEntries[0]);
 
@@ -57,17 +59,18 @@ cudaLaunchConfig_t cluster_config(const Entry& e, unsigned blocks, unsigned clus
     return cfg;
 }
 
-// ---------------------------------------------------------------- tile model --
+// ------------------------------------------------------------ pairs and splits --
 //
-// Time of a choice in SM clocks: waves of work units over the units that run at
-// once, each its K blocks times the clocks of one block plus a fixed part for
-// the tile's start and end. Of a block's clocks:
-//   tensor   4 MMAs of BN / 2 clocks
-//   L2       the stage's bytes at ~77 per clock and SM
-//   HBM      when B is streamed once (one m-tile): all units together draw
-//            ~2400 bytes per clock, one SM at most ~24
-// (the L2 and HBM rates are those measured for the block-scaled GEMMs).
-constexpr double kL2BytesPerClk = 77.0;
+// Every tile has 128 columns. Dense calls run on CTA pairs (256 rows) or single
+// CTAs, the grouped forms on single CTAs; K is split on single CTAs when the
+// output tiles leave SMs idle. The choice with the least modelled time, in clocks:
+//   waves x (K blocks of the longest range x clocks of a block + fixed clocks).
+// A block takes ~460 clocks on pairs and ~480 on single CTAs (4096x7168x16384:
+// 482 and 505 us; 4096x4096x7168: 119 and 123). With one m-tile the weights
+// stream from HBM: ~24 bytes per clock at most on one SM, ~2400 on all (as
+// measured for the block-scaled GEMMs).
+constexpr double kPairBlockClocks = 460.0;
+constexpr double kBlockClocks = 480.0;
 constexpr double kStreamBytesPerClk = 2400.0;
 constexpr double kStreamPerSmBytesPerClk = 24.0;
 constexpr double kTileClocks = 2000.0;
@@ -77,47 +80,43 @@ struct Choice {
     int entry, units, splits;
 };
 
-Choice choose(const Device& dev, int kind, bool rowb, int rows, int n, int kb, int64_t m_blocks) {
+Choice choose(const Device& dev, int kind, bool rowb, int epi, int rows, int n, int kb) {
     int forced_bn = 0, forced_cg = 0, forced_splits = 0;
     dg::host_forced_tile(&forced_bn, &forced_cg, &forced_splits);
-    if (kind != dg::kDense) forced_splits = 1;
-    if (kind == dg::kMasked) forced_cg = 0;
-    const int kg = (kb + 3) / 4;
     Choice best{-1, 0, 1};
+    if (forced_bn != 0 && forced_bn != dg::SF_F32_BN) return best;
+    if (kind == dg::kMasked) forced_cg = 0;  // always single CTAs, as the block-scaled form
+    if (kind != dg::kDense) forced_splits = 1;
+    const int kg = (kb + 3) / 4;
     double best_cost = 1e300;
     for (int i = 0; i < kNumEntries; ++i) {
         const Entry& e = kEntries[i];
-        if (e.kind != kind || e.rowb != rowb) continue;
-        if ((forced_bn != 0 && e.bn != forced_bn) || (forced_cg != 0 && e.cg != forced_cg)) continue;
-        if (forced_cg == 0 && forced_bn == 0 && e.cg == 2 && rows <= dg::BM) continue;  // half the pair would idle
+        if (e.kind != kind || e.rowb != rowb || e.epi != epi || (forced_cg != 0 && e.cg != forced_cg)) continue;
+        if (forced_cg == 0 && e.cg == 2 && rows <= dg::BM) continue;  // half of every pair would idle
         if (dev.units[i] < 1) continue;
-        const int64_t mt = (m_blocks + e.cg - 1) / e.cg;
-        const int64_t tiles = mt * ((n + e.bn - 1) / e.bn);
-        const int box = rows < dg::BM ? rows : dg::BM;
-        double clocks = 2.0 * e.bn;
-        const double l2 = (box + static_cast<double>(e.bn) / e.cg) * 128.0 / kL2BytesPerClk;
-        if (l2 > clocks) clocks = l2;
+        const int64_t mt = (static_cast<int64_t>(rows) + e.cg * dg::BM - 1) / (e.cg * dg::BM);
+        const int64_t tiles = mt * ((static_cast<int64_t>(n) + dg::SF_F32_BN - 1) / dg::SF_F32_BN);
         for (int s = 1; s <= dg::MAX_CLUSTER_SPLITS; ++s) {
             if (forced_splits != 0 && s != forced_splits) continue;
             int64_t units = dev.units[i];
             if (s > 1) {
-                if (kind != dg::kDense || e.cg != 1 || s > kg) break;
+                if (e.cg != 1 || s > kg) break;
+                if (forced_splits == 0 && tiles >= units) break;  // the tiles alone fill the GPU
                 units = static_cast<int64_t>(dev.clusters[i][s]) * s;
                 if (units < s) continue;
-                if (forced_splits == 0 && tiles >= dev.units[i]) break;  // the tiles alone fill the GPU
             }
             const int64_t work = tiles * s;
             const int64_t waves = (work + units - 1) / units;
-            double c = clocks;
+            double clocks = e.cg == 2 ? kPairBlockClocks : kBlockClocks;
             if (mt == 1) {
-                const double active = static_cast<double>(work < units ? work : units);
-                const double all = e.bn * 128.0 / e.cg * active * e.cg / kStreamBytesPerClk;
-                const double one = e.bn * 128.0 / e.cg / kStreamPerSmBytesPerClk;
-                if (all > c) c = all;
-                if (one > c) c = one;
+                const double bytes = dg::SF_F32_BN * 128.0;  // of B per tile and block
+                const double all = bytes * static_cast<double>(work < units ? work : units) / kStreamBytesPerClk;
+                const double one = bytes / e.cg / kStreamPerSmBytesPerClk;
+                if (all > clocks) clocks = all;
+                if (one > clocks) clocks = one;
             }
             const int blocks = 4 * ((kg + s - 1) / s) < kb ? 4 * ((kg + s - 1) / s) : kb;
-            const double cost = static_cast<double>(waves) * (blocks * c + kTileClocks + (s > 1 ? kSplitClocks : 0.0));
+            const double cost = static_cast<double>(waves) * (blocks * clocks + kTileClocks + (s > 1 ? kSplitClocks : 0.0));
             if (cost < best_cost * 0.999) {
                 best_cost = cost;
                 best = {i, static_cast<int>(units), s};
@@ -144,10 +143,10 @@ dg_status launch(int kind, SfF32Params& p, const void* a, const void* b, int64_t
     p.sfb_vec4 = p.kb % 4 == 0 && is_aligned(p.sfb32, 16);
     p.wait_limit_ns = dg::host_wait_limit_ns();
     p.test_mode = dg::host_test_mode();
-    const Choice choice = choose(dev, kind, sfb_gran_n == 1, p.rows, p.n, p.kb, m_blocks);
+    const Choice choice = choose(dev, kind, sfb_gran_n == 1, p.c != nullptr || p.out_f32, p.rows, p.n, p.kb);
     if (choice.entry < 0) return DG_ERR_UNSUPPORTED;  // a forced combination that is not built
     const Entry& e = kEntries[choice.entry];
-    p.num_n_blocks = (p.n + e.bn - 1) / e.bn;
+    p.num_n_blocks = (p.n + dg::SF_F32_BN - 1) / dg::SF_F32_BN;
     p.num_m_blocks = (p.rows + e.cg * dg::BM - 1) / (e.cg * dg::BM);
     p.raster_group = 16 / e.cg;  // bands of 2048 rows
     p.raster_shift = e.cg == 2 ? 3 : 4;
@@ -157,11 +156,11 @@ dg_status launch(int kind, SfF32Params& p, const void* a, const void* b, int64_t
     // a load brings no more rows of A than there are, in whole swizzle atoms of eight
     p.a_box_rows = p.rows >= dg::BM ? dg::BM : (p.rows + 7) / 8 * 8;
     if (!dg::host_encode_kmajor(&p.tma_a, a, kind == dg::kMasked ? 3 : 2, p.k, p.rows, a_mats, p.a_box_rows) ||
-        !dg::host_encode_kmajor(&p.tma_b, b, kind == dg::kDense ? 2 : 3, p.k, p.n, b_mats, e.sub_b_rows))
+        !dg::host_encode_kmajor(&p.tma_b, b, kind == dg::kDense ? 2 : 3, p.k, p.n, b_mats, e.b_rows))
         return DG_ERR_INVALID_ARG;
-    // work units: masked tiles are bounded by every group's m-blocks; contiguous pairs walk two passes
+    // work units: masked tiles are bounded by every group's m-blocks
     const int64_t m_tiles = kind == dg::kMasked ? m_blocks : p.num_m_blocks;
-    const int64_t tiles = m_tiles * p.num_n_blocks * choice.splits * (e.cg == 2 && kind == dg::kContiguous ? 2 : 1);
+    const int64_t tiles = m_tiles * p.num_n_blocks * choice.splits;
     if (tiles > (int64_t{1} << 30)) return DG_ERR_UNSUPPORTED;
     const bool split = choice.splits > 1;
     const int units = static_cast<int>(split || tiles < choice.units ? tiles : choice.units);
@@ -178,7 +177,7 @@ dg_status launch(int kind, SfF32Params& p, const void* a, const void* b, int64_t
     if (dg::host_log())
         std::fprintf(stderr, "[dgb200] fp32 scales, form=%d rows=%d N=%d K=%d groups=%d: BN=%d CTA-group=%d splits=%d grid=%d "
                              "smem=%d stages=%d\n",
-                     kind, p.rows, p.n, p.k, p.groups, e.bn, e.cg, choice.splits, units * e.cg, e.smem, e.stages);
+                     kind, p.rows, p.n, p.k, p.groups, dg::SF_F32_BN, e.cg, choice.splits, units * e.cg, e.smem, e.stages);
     void* args[] = {&p};
     return cudaLaunchKernelExC(&cfg, e.fn, args) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
@@ -186,7 +185,7 @@ dg_status launch(int kind, SfF32Params& p, const void* a, const void* b, int64_t
 dg_status check(const void* a, const float* sfa, const void* b, const float* sfb, const void* d, int rows, int N, int K) {
     if (!a || !sfa || !b || !sfb || !d || rows <= 0 || N <= 0 || K <= 0) return DG_ERR_INVALID_ARG;
     if (K % 128 != 0 || N % 8 != 0) return DG_ERR_INVALID_ARG;
-    if (K > (1 << 20)) return DG_ERR_UNSUPPORTED;
+    if (K > (1 << 20) || rows > (1 << 30) || N > (1 << 30)) return DG_ERR_UNSUPPORTED;
     if (!is_aligned(a, 16) || !is_aligned(b, 16) || !is_aligned(d, 16) || !is_aligned(sfa, 4) || !is_aligned(sfb, 4))
         return DG_ERR_ALIGNMENT;
     return DG_OK;

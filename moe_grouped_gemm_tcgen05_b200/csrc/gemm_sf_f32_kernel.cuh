@@ -10,28 +10,41 @@
 // accumulation inside the block), read back with tcgen05.ld and added to fp32
 // accumulators in registers with one FMA per element. Only D is rounded.
 //
-// What bounds it: the tensor core needs 4 x BN/2 clocks per 128-K block of a
-// 128 x BN tile (M = 128 rows per SM); reading the block back and the FMAs take
-// 128 x BN / 128 clocks each (128 lanes per SM), half of that, next to it. So
-// the tensor core stays the bound as long as the hand-offs between the two are
-// hidden, and the TMEM buffers (512 columns) are as many as fit.
+// What bounds it. A 128 x 128 product of one K-block is 4 MMAs of 64 clocks; the
+// epilogue's reads and FMAs take as long again next to them (8 warps: ~35 clocks
+// to read 64 columns each, ~130 to add them), and the hand-off of a product from
+// the MMAs to the epilogue and back ~280 clocks of latency in every warp
+// that takes part. The two meet at ~480 clocks a block, against 256 for the MMAs
+// alone. What that taught (clocks and times measured on one B200, 4096x7168x16384):
+//   - Next to one-wide FMAs the warp that issues MMAs starves: it shares its
+//     scheduler with FMAs that fill every issue slot, and 4 MMAs of N = 256 take
+//     890 clocks instead of 512. Two-wide FMAs leave every other slot free.
+//   - One warp issues 4 MMAs and a commit in ~300 clocks there, and waits for
+//     ~200; two warps take turns (647 -> 548 us with everything else equal).
+//   - Wider tiles (256 columns: two TMEM buffers) wait for the hand-off of
+//     a buffer, narrower ones do not: four buffers of 128 columns fit.
+//   - A warp's sums are all that its loop carries from block to block. Reading
+//     16 columns ahead across blocks cost ~200 clocks of register moves a block.
+//   - Scales loaded by the epilogue's warps themselves, even blocks ahead, held
+//     them up for ~300 clocks a block: a warp of its own brings them to shared
+//     memory (532 -> 505 us).
+//   - Two sets of warps that take every other block with all columns, and swap
+//     halves at the end, need 64 KB for the swap and leave too few stages in
+//     flight: 580 us.
 //
 // CTA = 12 warps (three warpgroups), one CTA per SM, persistent:
 //   warp 0      TMA producer (128-byte swizzle, STAGES-deep ring)
-//   warp 1      TMEM allocation and MMA issue
-//   warp 3      scales: (72 + 2 x 216 of the launch's 3 x 168 per lane)
+//   warps 1, 2  MMA issue, every other product each; warp 1 allocates TMEM
+//   warp 3      scale producer
 //   warps 4..   epilogue. Warp w reads TMEM lanes 32 (w % 4) .. + 31 (a row per
-//               lane) and owns half of the tile's columns, CW = BN / 2, whose
-//               accumulators stay in its registers over the whole K loop. 32
-//               columns are read from TMEM while the 32 before are added.
-// The tile's columns are NSUB sub-tiles with rings of TMEM buffers and barriers
-// of their own, so that a sub-tile's buffer is refilled NBUF blocks later while
-// the other sub-tiles' MMAs run.
+//               lane) and owns half of the tile's columns, whose sums stay in its
+//               registers over the whole K loop.
+// The first warpgroup gives registers to the other two (88 + 2 x 208 of the
+// launch's 3 x 168 per lane).
 //
-// CG = 2: a cluster of two CTAs computes 256 x BN (tcgen05 cta_group::2), which
-// halves the B bytes per SM: a lone CTA's 128 x 256 tile needs 48 KB of loads
-// per 512 clocks of math, more than the ~77 bytes per clock the L2 feeds an SM.
-// No load is multicast.
+// CG = 2 (dense): a cluster of two CTAs computes 256 x 128 (tcgen05 cta_group::2),
+// which takes B's loads from 16 to 8 KB a block and SM; the L2 feeds an SM about
+// 77 bytes per clock, so a lone CTA's 32 KB take ~425 clocks. No load is multicast.
 //
 // Split-K (dense, small M): the CTAs of a cluster take K ranges of one tile,
 // leave their fp32 partials in their own shared memory (the operand ring, idle
@@ -229,17 +242,16 @@ struct StoreRows {
 // warp's staging rows, 64 bytes of every row at a time: written back, four
 // lanes take the 64 bytes of a row. (Row-wise 16-byte stores straight from the
 // registers touch 32 rows per instruction and slow the operand loads.)
-template <int CW, int STG_ROW>
-__device__ __forceinline__ void store_rows(const GemmParams& p, const float* acc, const StoreRows& to,
+template <int CW, int STG_ROW, int EPI>
+__device__ __forceinline__ void store_rows(const GemmParams& p, const float (&acc)[CW], const StoreRows& to,
                                            int col0, uint8_t* stg, int lane) {
     const int sub = lane >> 2, piece = lane & 3;
-    if (p.c == nullptr && !p.out_f32) {
+    if constexpr (EPI == 0) {
 #pragma unroll
         for (int u = 0; u < CW; u += 32) {
-            const int pieces = (CW - u < 32 ? CW - u : 32) / 8;  // 16-byte pieces of eight bf16 columns
             __syncwarp();
 #pragma unroll
-            for (int q = 0; q < pieces; ++q) {
+            for (int q = 0; q < 4; ++q) {  // 16-byte pieces of eight bf16 columns
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -253,70 +265,74 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const float* acc
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int r = 8 * i + sub;
-                if (piece < pieces && col < p.n && ((to.rows >> r) & 1u))
+                if (col < p.n && ((to.rows >> r) & 1u))
                     *reinterpret_cast<uint4*>(p.d + (to.row0 + r) * p.n + col) =
                         *reinterpret_cast<const uint4*>(stg + r * STG_ROW + 16 * piece);
             }
         }
-        return;
-    }
-    // C and / or an fp32 D: 16 fp32 columns at a time
-#pragma unroll
-    for (int u = 0; u < CW; u += 16) {
-        const int pieces = (CW - u < 16 ? CW - u : 16) / 4;
-        __syncwarp();
-#pragma unroll
-        for (int q = 0; q < pieces; ++q) {
-            const int j = u + 4 * q;
-            *reinterpret_cast<float4*>(stg + lane * STG_ROW + 16 * q) =
-                make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-        }
-        __syncwarp();
-        const int col = col0 + u + 4 * piece;
-        const bool in = piece < pieces && col < p.n;
-        float4 c[4];
+    } else {
+        // C and / or an fp32 D: 16 fp32 columns at a time, all of C's loads issued first
+        float4 c[CW / 16][4];
         if (p.c != nullptr) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 8 * i + sub;
-                if (!in || !((to.rows >> r) & 1u)) continue;
-                const size_t at = (to.row0 + r) * p.n + col;
-                if (p.out_f32) {
-                    c[i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.c) + at);
-                } else {
-                    const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.c) + at);
-                    c[i] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
-                                       __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+            for (int u = 0; u < CW; u += 16) {
+                const int col = col0 + u + 4 * piece;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 8 * i + sub;
+                    if (col >= p.n || !((to.rows >> r) & 1u)) continue;
+                    const size_t at = (to.row0 + r) * p.n + col;
+                    if (p.out_f32) {
+                        c[u / 16][i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.c) + at);
+                    } else {
+                        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.c) + at);
+                        c[u / 16][i] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                                                   __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+                    }
                 }
             }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 8 * i + sub;
-            if (!in || !((to.rows >> r) & 1u)) continue;
-            const size_t at = (to.row0 + r) * p.n + col;
-            float4 v = *reinterpret_cast<const float4*>(stg + r * STG_ROW + 16 * piece);
-            if (p.c != nullptr) {
-                v.x += c[i].x;
-                v.y += c[i].y;
-                v.z += c[i].z;
-                v.w += c[i].w;
+        for (int u = 0; u < CW; u += 16) {
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int j = u + 4 * q;
+                *reinterpret_cast<float4*>(stg + lane * STG_ROW + 16 * q) =
+                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
             }
-            if (p.out_f32) {
-                *reinterpret_cast<float4*>(p.d32 + at) = v;
-            } else {
-                const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y), b1 = __floats2bfloat162_rn(v.z, v.w);
-                *reinterpret_cast<uint2*>(p.d + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&b0),
-                                                                 *reinterpret_cast<const uint32_t*>(&b1));
+            __syncwarp();
+            const int col = col0 + u + 4 * piece;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 8 * i + sub;
+                if (col >= p.n || !((to.rows >> r) & 1u)) continue;
+                const size_t at = (to.row0 + r) * p.n + col;
+                float4 v = *reinterpret_cast<const float4*>(stg + r * STG_ROW + 16 * piece);
+                if (p.c != nullptr) {
+                    v.x += c[u / 16][i].x;
+                    v.y += c[u / 16][i].y;
+                    v.z += c[u / 16][i].z;
+                    v.w += c[u / 16][i].w;
+                }
+                if (p.out_f32) {
+                    *reinterpret_cast<float4*>(p.d32 + at) = v;
+                } else {
+                    const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y), b1 = __floats2bfloat162_rn(v.z, v.w);
+                    *reinterpret_cast<uint2*>(p.d + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&b0),
+                                                                     *reinterpret_cast<const uint32_t*>(&b1));
+                }
             }
         }
     }
 }
 
-template <int KIND, int CG, bool ROWB>
+// EPI 1: the epilogue of C and / or an fp32 D; EPI 0: plain bf16 D. (The plain
+// one, compiled into one kernel with the other, lost 10% in its main loop.)
+template <int KIND, int CG, bool ROWB, int EPI>
 __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(const __grid_constant__ SfF32Params p) {
-    static_assert(CG == 1 || KIND != kMasked, "CTA pairs are built for the dense and contiguous forms");
-    static_assert(!ROWB || KIND == kDense, "per-row scales of B: dense form");
+    static_assert(CG == 1 || KIND == kDense, "CTA pairs are built for the dense form");
+    static_assert((!ROWB && EPI == 0) || KIND == kDense, "per-row scales of B, C and an fp32 D: dense form");
     using Cfg = SfF32Config<CG, sched_ints<KIND>(), ROWB>;
     constexpr int BN = Cfg::BN;
     constexpr int CW = Cfg::CW;
@@ -384,173 +400,173 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
     const int my_rows = BM * static_cast<int>(rank);
 
     if (warp < SF_F32_EPI_WARP0) {
-    registers_dec<SF_F32_OTHER_REGS>();
-    if (warp == 0) {
-        // -------------------------------------------------------- TMA producer --
-        [[maybe_unused]] uint32_t full_leader0 = 0;
-        if constexpr (CG == 2) full_leader0 = mapa_shared(smem_u32(&full_bar[0]), 0);
-        int stage = 0, issued = 0, gcur = 0;
-        uint32_t phase = 0;
-        Tile cur;
-        bool aborted = false;
-        const uint32_t tx = static_cast<uint32_t>(CG * (p.a_box_rows * BK + Cfg::B_BYTES));
-        for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
-             t += units) {
-            const int a_row = cur.m_blk * BM * CG + my_rows;
-            const int b_row = cur.n_blk * BN + Cfg::B_ROWS * static_cast<int>(rank);
-            const int g = max(cur.g, 0);
-            const int kb1 = min(4 * cur.kg1, p.kb);
-            for (int kb = 4 * cur.kg0; kb < kb1; ++kb) {
-                if (issued >= STAGES && !wait_warp(&done_bar[stage], phase ^ 1u, p, s_abort)) { aborted = true; break; }
-                // (the failure-path hook withholds CTA 0's first load)
-                if (elect_one() && !(p.test_mode == 1 && blockIdx.x == 0 && issued == 0)) {
-                    uint8_t* a_dst = smem_a + stage * Cfg::A_BYTES;
-                    uint8_t* b_dst = smem_b + stage * Cfg::B_BYTES;
-                    const int kx = kb * BK;
-                    if constexpr (CG == 1) {
-                        mbar_arrive_expect_tx(&full_bar[stage], tx);
-                        if constexpr (KIND == kMasked) tma_load_3d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row, g);
-                        else tma_load_2d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row);
-                    } else {
-                        // both CTAs' loads complete on the leader's barrier
-                        if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
-                        tma_load_2d_pair(a_dst, &p.tma_a, full_leader0 + 8u * static_cast<uint32_t>(stage), kx, a_row);
+        registers_dec<SF_F32_OTHER_REGS>();
+        if (warp == 0) {
+            // -------------------------------------------------------- TMA producer --
+            [[maybe_unused]] uint32_t full_leader0 = 0;
+            if constexpr (CG == 2) full_leader0 = mapa_shared(smem_u32(&full_bar[0]), 0);
+            int stage = 0, issued = 0, gcur = 0;
+            uint32_t phase = 0;
+            Tile cur;
+            bool aborted = false;
+            const uint32_t tx = static_cast<uint32_t>(CG * (p.a_box_rows * BK + Cfg::B_BYTES));
+            for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
+                 t += units) {
+                const int a_row = cur.m_blk * BM * CG + my_rows;
+                const int b_row = cur.n_blk * BN + Cfg::B_ROWS * static_cast<int>(rank);
+                const int g = max(cur.g, 0);
+                const int kb1 = min(4 * cur.kg1, p.kb);
+                for (int kb = 4 * cur.kg0; kb < kb1; ++kb) {
+                    if (issued >= STAGES && !wait_warp(&done_bar[stage], phase ^ 1u, p, s_abort)) { aborted = true; break; }
+                    // (the failure-path hook withholds CTA 0's first load)
+                    if (elect_one() && !(p.test_mode == 1 && blockIdx.x == 0 && issued == 0)) {
+                        uint8_t* a_dst = smem_a + stage * Cfg::A_BYTES;
+                        uint8_t* b_dst = smem_b + stage * Cfg::B_BYTES;
+                        const int kx = kb * BK;
+                        if constexpr (CG == 1) {
+                            mbar_arrive_expect_tx(&full_bar[stage], tx);
+                            if constexpr (KIND == kMasked) tma_load_3d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row, g);
+                            else tma_load_2d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row);
+                        } else {
+                            // both CTAs' loads complete on the leader's barrier
+                            if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
+                            tma_load_2d_pair(a_dst, &p.tma_a, full_leader0 + 8u * static_cast<uint32_t>(stage), kx, a_row);
+                        }
+                        if constexpr (CG == 1) {
+                            if constexpr (KIND == kDense) tma_load_2d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row);
+                            else tma_load_3d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row, g);
+                        } else {
+                            const uint32_t fb = full_leader0 + 8u * static_cast<uint32_t>(stage);
+                            if constexpr (KIND == kDense) tma_load_2d_pair(b_dst, &p.tma_b, fb, kx, b_row);
+                            else tma_load_3d_pair(b_dst, &p.tma_b, fb, kx, b_row, g);
+                        }
                     }
-                    if constexpr (CG == 1) {
-                        if constexpr (KIND == kDense) tma_load_2d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row);
-                        else tma_load_3d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row, g);
-                    } else {
-                        const uint32_t fb = full_leader0 + 8u * static_cast<uint32_t>(stage);
-                        if constexpr (KIND == kDense) tma_load_2d_pair(b_dst, &p.tma_b, fb, kx, b_row);
-                        else tma_load_3d_pair(b_dst, &p.tma_b, fb, kx, b_row, g);
+                    __syncwarp();
+                    ++issued;
+                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                }
+            }
+            if (aborted) {
+                // let the loads already issued land before shared memory goes away
+                if constexpr (CG == 1) {
+                    int s = stage;
+                    uint32_t ph = phase;
+                    for (int i = 0; i < STAGES && i < issued; ++i) {
+                        if (--s < 0) { s = STAGES - 1; ph ^= 1u; }
+                        wait_quiet(&full_bar[s], ph, p.wait_limit_ns / 16);
+                    }
+                } else {
+                    sleep_ns(p.wait_limit_ns / 16);
+                }
+            }
+        } else if (warp <= SF_F32_ISSUERS) {
+            // --------------------------------------------------------- MMA issuers --
+            // Block products are dealt out in turn: two waits, four MMAs and two
+            // commits take a lone warp ~450 clocks next to the epilogue's warps,
+            // longer than the MMAs run.
+            if (CG == 1 || leader) {
+                const uint32_t mine = warp - 1;
+                const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem_a));
+                const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem_b));
+                const uint32_t full0 = smem_u32(full_bar), tempty0 = smem_u32(tempty_bar), done0 = smem_u32(done_bar);
+                int gcur = 0;
+                uint32_t item0 = 0;   // block products before this tile
+                uint32_t stage = mine, par = 0;   // of this warp's next product
+                Tile c;
+                bool aborted = false;
+                for (int t = unit; !aborted && next_tile<KIND, CG == 2, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+                     t += units) {
+                    const uint32_t n = static_cast<uint32_t>(min(4 * c.kg1, p.kb) - 4 * c.kg0);
+                    // the products whose number has this warp's parity
+                    for (uint32_t it = item0 + ((item0 ^ mine) & 1u); it < item0 + n; it += 2) {
+                        // operands landed, and the buffer's last product read back: both probes at once
+                        const uint32_t buf = it % NBUF, buf_par = ((it / NBUF) & 1u) ^ 1u;
+                        const bool ready = mbar_try_wait_addr(full0 + 8 * stage, par) & mbar_try_wait_addr(tempty0 + 8 * buf, buf_par);
+                        if (!__all_sync(0xffffffffu, ready) && !(wait_warp(&full_bar[stage], par, p, s_abort) &&
+                                                                wait_warp(&tempty_bar[buf], buf_par, p, s_abort))) {
+                            aborted = true;
+                            break;
+                        }
+                        tc_fence_after();  // the epilogue's reads of this buffer precede the MMAs below
+                        const uint64_t adesc = adesc0 + stage * (Cfg::A_BYTES >> 4), bdesc = bdesc0 + stage * (Cfg::B_BYTES >> 4);
+                        if (elect_one()) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                tc_mma_f8<CG>(tmem_base + buf * BN, adesc + 2 * k, bdesc + 2 * k, Cfg::IDESC, k > 0 ? 1u : 0u);
+                            tc_commit_addr<CG>(done0 + 8 * stage);
+                        }
+                        __syncwarp();
+                        stage += 2;
+                        if (stage >= STAGES) { stage -= STAGES; par ^= 1u; }
+                    }
+                    item0 += n;
+                }
+                if (elect_one()) tc_commit<CG>(drain_bar);
+                __syncwarp();
+            }
+            wait_quiet(drain_bar, 0, p.wait_limit_ns);
+        } else {
+            // ------------------------------------------------------ scale producer --
+            // Gathers the scales of four K-blocks of every row (lane l: rows l, l + 32,
+            // ...) into shared memory, the next four K-blocks' loads in flight. (Read
+            // by the epilogue's warps from global memory, even several blocks ahead,
+            // the scales held them up for ~300 clocks a block.)
+            float a[2][4][4], b[2][ROWB ? 4 : 1][4];   // [set][row][K-block]
+            auto load4 = [&](const float* row, int kb0, bool vec, float (&v)[4]) {
+                if (vec) {
+                    ld_scale4(row + kb0, v);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) v[i] = ld_scale(row + min(kb0 + i, p.kb - 1));
+                }
+            };
+            uint32_t stored = 0;
+            auto store = [&](int set) {
+                const uint32_t slot = stored % Cfg::SF_SLOTS;
+                if (!wait_block(&sempty_bar[slot], ((stored / Cfg::SF_SLOTS) & 1u) ^ 1u, p, s_abort)) return false;
+                float* dst = smem_sf + slot * Cfg::SF_SLOT_FLOATS + lane;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        dst[i * BM + 32 * j] = ROWB ? a[set][j][i] : a[set][j][i] * b[set][0][i];
+                        if constexpr (ROWB) dst[4 * BM + i * BN + 32 * j] = b[set][j][i];
                     }
                 }
                 __syncwarp();
-                ++issued;
-                if (++stage == STAGES) { stage = 0; phase ^= 1u; }
-            }
-        }
-        if (aborted) {
-            // let the loads already issued land before shared memory goes away
-            if constexpr (CG == 1) {
-                int s = stage;
-                uint32_t ph = phase;
-                for (int i = 0; i < STAGES && i < issued; ++i) {
-                    if (--s < 0) { s = STAGES - 1; ph ^= 1u; }
-                    wait_quiet(&full_bar[s], ph, p.wait_limit_ns / 16);
-                }
-            } else {
-                sleep_ns(p.wait_limit_ns / 16);
-            }
-        }
-    } else if (warp <= SF_F32_ISSUERS) {
-        // --------------------------------------------------------- MMA issuers --
-        // Block products are dealt out in turn: two waits, four MMAs and two
-        // commits take a lone warp ~450 clocks next to the epilogue's warps,
-        // longer than the MMAs run.
-        if (CG == 1 || leader) {
-            const uint32_t mine = warp - 1;
-            const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem_a));
-            const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem_b));
-            const uint32_t full0 = smem_u32(full_bar), tempty0 = smem_u32(tempty_bar), done0 = smem_u32(done_bar);
+                if (lane == 0) mbar_arrive(&sfull_bar[slot]);
+                ++stored;
+                return true;
+            };
             int gcur = 0;
-            uint32_t item0 = 0;   // block products before this tile
-            uint32_t stage = mine, par = 0;   // of this warp's next product
             Tile c;
             bool aborted = false;
-            for (int t = unit; !aborted && next_tile<KIND, CG == 2, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+            for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
                  t += units) {
-                const uint32_t n = static_cast<uint32_t>(min(4 * c.kg1, p.kb) - 4 * c.kg0);
-                // the products whose number has this warp's parity
-                for (uint32_t it = item0 + ((item0 ^ mine) & 1u); it < item0 + n; it += 2) {
-                    // operands landed, and the buffer's last product read back: both probes at once
-                    const uint32_t buf = it % NBUF, buf_par = ((it / NBUF) & 1u) ^ 1u;
-                    const bool ready = mbar_try_wait_addr(full0 + 8 * stage, par) & mbar_try_wait_addr(tempty0 + 8 * buf, buf_par);
-                    if (!__all_sync(0xffffffffu, ready) && !(wait_warp(&full_bar[stage], par, p, s_abort) &&
-                                                            wait_warp(&tempty_bar[buf], buf_par, p, s_abort))) {
-                        aborted = true;
-                        break;
+                // rows and columns clamped into the operands (those past them are never stored)
+                const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
+                const int row0 = c.m_blk * BM * CG + my_rows + static_cast<int>(lane);
+                const float* sfb = p.sfb32 + static_cast<size_t>(KIND == kDense ? 0 : max(c.g, 0)) * p.nb_sf * p.kb;
+                auto load = [&](int set, int kg) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        load4(p.sfa32 + (a_base + min(row0 + 32 * j, p.rows - 1)) * p.kb, 4 * kg, p.sfa_vec4 != 0, a[set][j]);
+#pragma unroll
+                    for (int j = 0; j < (ROWB ? 4 : 1); ++j) {
+                        const int row = ROWB ? min(c.n_blk * BN + 32 * j + static_cast<int>(lane), p.n - 1) : c.n_blk;
+                        load4(sfb + static_cast<size_t>(row) * p.kb, 4 * kg, p.sfb_vec4 != 0, b[set][j]);
                     }
-                    tc_fence_after();  // the epilogue's reads of this buffer precede the MMAs below
-                    const uint64_t adesc = adesc0 + stage * (Cfg::A_BYTES >> 4), bdesc = bdesc0 + stage * (Cfg::B_BYTES >> 4);
-                    if (elect_one()) {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            tc_mma_f8<CG>(tmem_base + buf * BN, adesc + 2 * k, bdesc + 2 * k, Cfg::IDESC, k > 0 ? 1u : 0u);
-                        tc_commit_addr<CG>(done0 + 8 * stage);
-                    }
-                    __syncwarp();
-                    stage += 2;
-                    if (stage >= STAGES) { stage -= STAGES; par ^= 1u; }
+                };
+                load(0, c.kg0);
+                for (int kg = c.kg0; kg < c.kg1; kg += 2) {
+                    if (kg + 1 < c.kg1) load(1, kg + 1);
+                    if (!store(0)) { aborted = true; break; }
+                    if (kg + 1 >= c.kg1) break;
+                    if (kg + 2 < c.kg1) load(0, kg + 2);
+                    if (!store(1)) { aborted = true; break; }
                 }
-                item0 += n;
-            }
-            if (elect_one()) tc_commit<CG>(drain_bar);
-            __syncwarp();
-        }
-        wait_quiet(drain_bar, 0, p.wait_limit_ns);
-    } else {
-        // ------------------------------------------------------ scale producer --
-        // Gathers the scales of four K-blocks of every row (lane l: rows l, l + 32,
-        // ...) into shared memory, the next four K-blocks' loads in flight. (Read
-        // by the epilogue's warps from global memory, even several blocks ahead,
-        // the scales held them up for ~300 clocks a block.)
-        float a[2][4][4], b[2][ROWB ? 4 : 1][4];   // [set][row][K-block]
-        auto load4 = [&](const float* row, int kb0, bool vec, float (&v)[4]) {
-            if (vec) {
-                ld_scale4(row + kb0, v);
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = ld_scale(row + min(kb0 + i, p.kb - 1));
-            }
-        };
-        uint32_t stored = 0;
-        auto store = [&](int set) {
-            const uint32_t slot = stored % Cfg::SF_SLOTS;
-            if (!wait_block(&sempty_bar[slot], ((stored / Cfg::SF_SLOTS) & 1u) ^ 1u, p, s_abort)) return false;
-            float* dst = smem_sf + slot * Cfg::SF_SLOT_FLOATS + lane;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    dst[i * BM + 32 * j] = ROWB ? a[set][j][i] : a[set][j][i] * b[set][0][i];
-                    if constexpr (ROWB) dst[4 * BM + i * BN + 32 * j] = b[set][j][i];
-                }
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sfull_bar[slot]);
-            ++stored;
-            return true;
-        };
-        int gcur = 0;
-        Tile c;
-        bool aborted = false;
-        for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
-             t += units) {
-            // rows and columns clamped into the operands (those past them are never stored)
-            const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
-            const int row0 = c.m_blk * BM * CG + my_rows + static_cast<int>(lane);
-            const float* sfb = p.sfb32 + static_cast<size_t>(KIND == kDense ? 0 : max(c.g, 0)) * p.nb_sf * p.kb;
-            auto load = [&](int set, int kg) {
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    load4(p.sfa32 + (a_base + min(row0 + 32 * j, p.rows - 1)) * p.kb, 4 * kg, p.sfa_vec4 != 0, a[set][j]);
-#pragma unroll
-                for (int j = 0; j < (ROWB ? 4 : 1); ++j) {
-                    const int row = ROWB ? min(c.n_blk * BN + 32 * j + static_cast<int>(lane), p.n - 1) : c.n_blk;
-                    load4(sfb + static_cast<size_t>(row) * p.kb, 4 * kg, p.sfb_vec4 != 0, b[set][j]);
-                }
-            };
-            load(0, c.kg0);
-            for (int kg = c.kg0; kg < c.kg1; kg += 2) {
-                if (kg + 1 < c.kg1) load(1, kg + 1);
-                if (!store(0)) { aborted = true; break; }
-                if (kg + 1 >= c.kg1) break;
-                if (kg + 2 < c.kg1) load(0, kg + 2);
-                if (!store(1)) { aborted = true; break; }
             }
         }
-    }
     } else {
         registers_inc<SF_F32_EPI_REGS>();
         // ------------------------------------------------------------ epilogue --
@@ -648,12 +664,11 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 const int id = mloc < p.rows ? __ldg(p.meta + mloc) : -1;
                 const bool in_range = id >= 0 && id < p.groups;
                 valid = in_range && id == c.g;
-                const int own = rank == 0 ? c.e_own[0] : c.e_own[1];
-                if (in_range && id != own) atomicOr(p.status, DEVERR_MIXED_EXPERT_BLOCK);
+                if (in_range && id != c.g) atomicOr(p.status, DEVERR_MIXED_EXPERT_BLOCK);
             }
             to.rows = __ballot_sync(0xffffffffu, valid);
             if (to.rows != 0)
-                store_rows<CW, Cfg::STG_ROW>(p, acc, to, c.n_blk * BN + grp * CW, stg, static_cast<int>(lane));
+                store_rows<CW, Cfg::STG_ROW, EPI>(p, acc, to, c.n_blk * BN + grp * CW, stg, static_cast<int>(lane));
         }
     }
 
@@ -683,7 +698,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                         sum[0] += lo.x; sum[1] += lo.y; sum[2] += lo.z; sum[3] += lo.w;
                         sum[4] += hi.x; sum[5] += hi.y; sum[6] += hi.z; sum[7] += hi.w;
                     }
-                    cluster_store8<1>(p, sum, (static_cast<size_t>(c.m_blk) * BM + row) * p.n + col);
+                    cluster_store8<EPI>(p, sum, (static_cast<size_t>(c.m_blk) * BM + row) * p.n + col);
                 }
             }
         }

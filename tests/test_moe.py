@@ -186,7 +186,7 @@ def test_sf_f32_gemm_refusals(lib):
         for kw in (dict(a=None), dict(sfa=None), dict(b=None), dict(sfb=None), dict(d=None), dict(M=0), dict(N=0),
                    dict(K=0), dict(K=100), dict(N=12)):
             assert call(**kw) == 1, kw
-        assert call(K=(1 << 20) + 128) == 3
+        assert call(K=(1 << 20) + 128) == 3 and call(M=(1 << 30) + 1) == 3 and call(N=(1 << 30) + 8) == 3
         for name in ("a", "b", "d"):
             assert call(**{name: VP(0x10008)}) == 2
         assert call(sfa=VP(0x10002)) == 2 and call(sfb=VP(0x10001)) == 2
