@@ -146,12 +146,19 @@ def _check(fn: str, status: int):
         raise DgError(fn, status)
 
 
-def _stream():
-    return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+# The handle of torch's current stream as a number. (current_stream() builds a
+# Stream object around it on every call: ~1.5 us of a call's ~10.)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream(device=None):
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device() if device is None else device)
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _ptr(t: torch.Tensor):
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()  # ctypes turns it into the void* that the signatures declare
 
 
 def _need(t: torch.Tensor, name: str, dtypes, shape=None):
@@ -163,7 +170,7 @@ def _need(t: torch.Tensor, name: str, dtypes, shape=None):
         raise TypeError(f"{name} has dtype {t.dtype}, expected one of {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:  # a torch.Size compares as the tuple it is
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
 
 
@@ -497,12 +504,18 @@ _LOGITS = (torch.float32, torch.bfloat16)
 _SCORES = {"softmax": 0, "sigmoid": 1}
 
 
+def _new(shape, dtype, device):
+    """torch.empty of a matrix or vector, a third quicker (a decode step's calls are bound by such things)."""
+    return torch.empty_strided(shape, (shape[1], 1) if len(shape) == 2 else (1,), dtype=dtype, device=device)
+
+
 def _here(*tensors):
-    """All tensors live on the current device: the call runs on its stream."""
+    """The handle of the current device's current stream; all tensors live on that device."""
     device = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != device:
+        if t is not None and t.get_device() != device:
             raise ValueError(f"a tensor is on {t.device}, but the current device is cuda:{device}")
+    return _stream(device)
 
 
 def _score(score):
@@ -527,16 +540,16 @@ def moe_route(logits, k, *, bias=None, score="softmax", n_groups=1, top_groups=1
     if bias is not None:
         _need(bias, "bias", _F32, (E,))
     if ids is None:
-        ids = torch.empty((T, max(k, 0)), dtype=torch.int32, device=logits.device)
+        ids = _new((T, max(k, 0)), torch.int32, logits.device)
     if weights is None:
-        weights = torch.empty((T, max(k, 0)), dtype=torch.float32, device=logits.device)
+        weights = _new((T, max(k, 0)), torch.float32, logits.device)
     _need(ids, "ids", _I32, (T, k))
     _need(weights, "weights", _F32, (T, k))
-    _here(logits, bias, ids, weights)
+    stream = _here(logits, bias, ids, weights)
     _check("moe_route",
            load().moe_route(_ptr(logits), int(logits.dtype == torch.float32), _opt(bias), _ptr(ids), _ptr(weights), T, E,
                             k, _score(score), int(n_groups), int(top_groups), int(group_top), int(bool(renormalize)),
-                            float(scale), _stream()))
+                            float(scale), stream))
     return ids, weights
 
 
@@ -553,11 +566,11 @@ def moe_route_backward(logits, ids, d_weights, *, score="softmax", renormalize=T
     if d_logits is None:
         d_logits = torch.empty_like(logits)
     _need(d_logits, "d_logits", (logits.dtype,), (T, E))
-    _here(logits, ids, d_weights, d_logits)
+    stream = _here(logits, ids, d_weights, d_logits)
     _check("moe_route_backward",
            load().moe_route_backward(_ptr(logits), int(logits.dtype == torch.float32), _ptr(ids), _ptr(d_weights),
                                      _ptr(d_logits), T, E, k, _score(score), int(bool(renormalize)), float(scale),
-                                     _stream()))
+                                     stream))
     return d_logits
 
 
@@ -573,7 +586,7 @@ def _rows_args(ids, G, row_of, counts):
     if row_of is None:
         row_of = torch.empty_like(ids)
     if counts is None:
-        counts = torch.empty((max(int(G), 0),), dtype=torch.int32, device=ids.device)
+        counts = _new((max(int(G), 0),), torch.int32, ids.device)
     _need(row_of, "row_of", _I32, ids.shape)
     _need(counts, "counts", _I32, (G,))
     return row_of, counts
@@ -586,12 +599,12 @@ def moe_rows_contiguous(ids, G, *, row_of=None, m_indices=None, counts=None):
     row_of, counts = _rows_args(ids, G, row_of, counts)
     T, k = ids.shape
     if m_indices is None:
-        m_indices = torch.empty((moe_rows_bound(T, k, G),), dtype=torch.int32, device=ids.device)
+        m_indices = _new((moe_rows_bound(T, k, G),), torch.int32, ids.device)
     _need(m_indices, "m_indices", _I32, (m_indices.numel(),))
-    _here(ids, row_of, m_indices, counts)
+    stream = _here(ids, row_of, m_indices, counts)
     _check("moe_rows_contiguous",
            load().moe_rows_contiguous(_ptr(ids), _ptr(row_of), _ptr(m_indices), _ptr(counts), T, k, int(G),
-                                      m_indices.numel(), _stream()))
+                                      m_indices.numel(), stream))
     return row_of, m_indices, counts
 
 
@@ -601,12 +614,12 @@ def moe_rows_masked(ids, G, max_m, *, row_of=None, masked_m=None, counts=None):
     row_of, counts = _rows_args(ids, G, row_of, counts)
     T, k = ids.shape
     if masked_m is None:
-        masked_m = torch.empty((G,), dtype=torch.int32, device=ids.device)
+        masked_m = _new((G,), torch.int32, ids.device)
     _need(masked_m, "masked_m", _I32, (G,))
-    _here(ids, row_of, masked_m, counts)
+    stream = _here(ids, row_of, masked_m, counts)
     _check("moe_rows_masked",
            load().moe_rows_masked(_ptr(ids), _ptr(row_of), _ptr(masked_m), _ptr(counts), T, k, int(G), int(max_m),
-                                  _stream()))
+                                  stream))
     return row_of, masked_m, counts
 
 
@@ -631,10 +644,10 @@ def moe_dispatch_fp8(x, row_of, q, sf):
     _need(sf, "sf", (torch.int32, torch.float32))
     sf_f32 = sf.dtype == torch.float32
     _need(sf, "sf", (sf.dtype,), (*q.shape[:-1], H // BLOCK if sf_f32 else _kp(H)))
-    _here(x, row_of, q, sf)
+    stream = _here(x, row_of, q, sf)
     _check("moe_dispatch_fp8",
            load().moe_dispatch_fp8(_ptr(x), int(x.dtype == torch.float32), _ptr(row_of), _ptr(q), _ptr(sf), int(sf_f32),
-                                   rows, T, row_of.shape[1], H, _stream()))
+                                   rows, T, row_of.shape[1], H, stream))
     return q, sf
 
 
@@ -643,15 +656,15 @@ def quantize_fp8_1x128_sf_f32(x, q=None, sf=None):
     _need(x, "x", _LOGITS)
     rows, K = x.shape
     if q is None:
-        q = torch.empty((rows, K), dtype=torch.uint8, device=x.device)
+        q = _new((rows, K), torch.uint8, x.device)
     if sf is None:
-        sf = torch.empty((rows, K // BLOCK), dtype=torch.float32, device=x.device)
+        sf = _new((rows, K // BLOCK), torch.float32, x.device)
     _need(q, "q", _FP8, (rows, K))
     _need(sf, "sf", _F32, (rows, K // BLOCK))
-    _here(x, q, sf)
+    stream = _here(x, q, sf)
     _check("quantize_fp8_1x128_sf_f32",
            load().quantize_fp8_1x128_sf_f32(_ptr(x), int(x.dtype == torch.float32), _ptr(q), _ptr(sf), rows, K,
-                                            _stream()))
+                                            stream))
     return q, sf
 
 
@@ -673,10 +686,10 @@ def moe_combine(y, row_of, weights=None, out=None):
     [G, max_m, H] bf16; slots with row -1 add nothing; weights None means ones."""
     rows, T, k, H = _combine_args(y, row_of, weights)
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=y.device)
+        out = _new((T, H), torch.bfloat16, y.device)
     _need(out, "out", _BF16, (T, H))
-    _here(y, row_of, weights, out)
-    _check("moe_combine", load().moe_combine(_ptr(y), _ptr(row_of), _opt(weights), _ptr(out), rows, T, k, H, _stream()))
+    stream = _here(y, row_of, weights, out)
+    _check("moe_combine", load().moe_combine(_ptr(y), _ptr(row_of), _opt(weights), _ptr(out), rows, T, k, H, stream))
     return out
 
 
@@ -687,12 +700,12 @@ def moe_combine_backward(y, row_of, weights, d_out, d_y, d_weights=None):
     _need(d_out, "d_out", _BF16, (T, H))
     _need(d_y, "d_y", _BF16, y.shape)
     if d_weights is None:
-        d_weights = torch.empty((T, k), dtype=torch.float32, device=y.device)
+        d_weights = _new((T, k), torch.float32, y.device)
     _need(d_weights, "d_weights", _F32, (T, k))
-    _here(y, row_of, weights, d_out, d_y, d_weights)
+    stream = _here(y, row_of, weights, d_out, d_y, d_weights)
     _check("moe_combine_backward",
            load().moe_combine_backward(_ptr(y), _ptr(row_of), _opt(weights), _ptr(d_out), _ptr(d_y), _ptr(d_weights),
-                                       rows, T, k, H, _stream()))
+                                       rows, T, k, H, stream))
     return d_y, d_weights
 
 
@@ -712,10 +725,10 @@ def fp8_gemm_nt_sf_f32(a, sfa, b, sfb, d, c=None, sfb_gran_n: int = BLOCK):
     _need(d, "d", (torch.bfloat16, torch.float32), (M, N))
     if c is not None:
         _need(c, "c", (d.dtype,), (M, N))
-    _here(a, sfa, b, sfb, d, c)
+    stream = _here(a, sfa, b, sfb, d, c)
     _check("fp8_gemm_nt_sf_f32",
            load().fp8_gemm_nt_sf_f32(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), int(sfb_gran_n), _opt(c), _ptr(d), M, N, K,
-                                     int(d.dtype == torch.float32), _stream()))
+                                     int(d.dtype == torch.float32), stream))
     return d
 
 
@@ -731,10 +744,10 @@ def m_grouped_fp8_gemm_nt_contiguous_sf_f32(a, sfa, b, sfb, d, m_indices):
     _need(sfb, "sfb", _F32, (G, _sfb_rows(N, BLOCK), K // BLOCK))
     _need(d, "d", _BF16, (M_total, N))
     _need(m_indices, "m_indices", _I32, (M_total,))
-    _here(a, sfa, b, sfb, d, m_indices)
+    stream = _here(a, sfa, b, sfb, d, m_indices)
     _check("m_grouped_fp8_gemm_nt_contiguous_sf_f32",
            load().m_grouped_fp8_gemm_nt_contiguous_sf_f32(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d),
-                                                          _ptr(m_indices), M_total, N, K, G, _stream()))
+                                                          _ptr(m_indices), M_total, N, K, G, stream))
     return d
 
 
@@ -750,8 +763,8 @@ def m_grouped_fp8_gemm_nt_masked_sf_f32(a, sfa, b, sfb, d, masked_m):
     _need(sfb, "sfb", _F32, (G, _sfb_rows(N, BLOCK), K // BLOCK))
     _need(d, "d", _BF16, (G, max_m, N))
     _need(masked_m, "masked_m", _I32, (G,))
-    _here(a, sfa, b, sfb, d, masked_m)
+    stream = _here(a, sfa, b, sfb, d, masked_m)
     _check("m_grouped_fp8_gemm_nt_masked_sf_f32",
            load().m_grouped_fp8_gemm_nt_masked_sf_f32(_ptr(a), _ptr(sfa), _ptr(b), _ptr(sfb), _ptr(d), _ptr(masked_m),
-                                                      G, max_m, N, K, _stream()))
+                                                      G, max_m, N, K, stream))
     return d

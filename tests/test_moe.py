@@ -215,8 +215,12 @@ def test_binding_refusals():
 def test_binding_refuses_another_device(monkeypatch):
     class On:
         def __init__(self, index):
-            self.device = type("D", (), {"index": index, "__str__": lambda s: f"cuda:{index}"})()
+            self.index, self.device = index, f"cuda:{index}"
+
+        def get_device(self):
+            return self.index
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    dg._here(On(0), None, On(0))
+    monkeypatch.setattr(dg, "_stream", lambda device: 7)
+    assert dg._here(On(0), None, On(0)) == 7
     with pytest.raises(ValueError, match="cuda:1"):
         dg._here(On(0), On(1))
