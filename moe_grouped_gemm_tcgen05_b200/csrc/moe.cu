@@ -70,9 +70,11 @@ dg_status check_route_sizes(int T, int E, int k) {
     return DG_OK;
 }
 
-unsigned route_blocks(int T) {
+// A warp per token; `cap` bounds the blocks (0: none), whose warps then take several.
+unsigned route_blocks(int T, int64_t cap) {
     const int per = dg::ROUTE_THREADS / 32;
-    return static_cast<unsigned>((static_cast<int64_t>(T) + per - 1) / per);
+    const int64_t n = (static_cast<int64_t>(T) + per - 1) / per;
+    return static_cast<unsigned>(cap > 0 && n > cap ? cap : n);
 }
 
 // One cluster for n choices: a single CTA while its warps have little to
@@ -167,7 +169,8 @@ dg_status moe_route(const void* logits, int logits_f32, const float* bias, int32
                             group_top < size ? group_top : size, score == DG_SCORE_SOFTMAX ? 1 : 0, renormalize, scale};
     const int v = lane_experts(E);
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = dg::host_launch(route_blocks(T), dg::ROUTE_THREADS, 0, stream, attr);
+    const cudaLaunchConfig_t cfg =
+        dg::host_launch(route_blocks(T, static_cast<int64_t>(dev.sms) * 4), dg::ROUTE_THREADS, 0, stream, attr);
     return launched(cudaLaunchKernelEx(&cfg, logits_f32 ? route_fn<true>(v) : route_fn<false>(v), p));
 }
 
@@ -189,7 +192,7 @@ dg_status moe_route_backward(const void* logits, int logits_f32, const int32_t* 
                                     renormalize, scale};
     const int v = lane_experts(E);
     cudaLaunchAttribute attr[2];
-    const cudaLaunchConfig_t cfg = dg::host_launch(route_blocks(T), dg::ROUTE_THREADS, 0, stream, attr);
+    const cudaLaunchConfig_t cfg = dg::host_launch(route_blocks(T, 0), dg::ROUTE_THREADS, 0, stream, attr);
     return launched(cudaLaunchKernelEx(&cfg, logits_f32 ? route_backward_fn<true>(v) : route_backward_fn<false>(v), p));
 }
 

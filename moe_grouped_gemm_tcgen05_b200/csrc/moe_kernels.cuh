@@ -28,18 +28,25 @@ constexpr float ROUTE_EPS = 1e-20f;    // added to the sum that weights are divi
 // top_groups best stay; ids are the k largest keys left, ties to the lowest
 // index; weights are scale * s[ids], divided by their sum when renormalised.
 //
-// One warp per token, expert e = lane * V + i in register i of its lane, so
-// the lowest lane and register of equal keys is the lowest index, and a group
-// is a run of lanes whenever its size is V times a power of two.
+// One warp per token, expert e = lane * V + i in register i of its lane, so a
+// group is a run of lanes whenever its size is V times a power of two.
 //
-// Two keys can lie closer than fp32 resolves (16384 tokens of 256 experts
-// hold a few such pairs), and the choice must not depend on the rounding of a
-// fast exponential. So keys are computed in fp32 (error below ROUTE_TOL / 4),
-// and a token where two neighbours of the sorted choice, or two groups, lie
-// within ROUTE_TOL is ranked again in fp64. Without a bias the logits
-// themselves rank like the scores and no token needs that.
-
-constexpr float ROUTE_TOL = 4e-6f;
+// What bounds it: instructions. A token is ~1 KB of logits, and its choice ~500
+// warp instructions with the following representation (1824 with keys and
+// indices apart: 45 us for 16384 tokens of 256 experts, against the memory's
+// 2.6). A key is an unsigned integer that orders like the fp32 value, with
+// the complement of the register's index in its lowest bits; a lane's keys are
+// sorted once, a round takes the largest first key of all lanes (one reduction),
+// and its lane moves up.
+//
+// Two keys can lie closer than that resolves, or than fp32 does (16384 tokens of
+// 256 experts hold a few such pairs), and the choice must not depend on the
+// rounding of a fast exponential. So a token where two neighbours of the sorted
+// choice, or the last group that stays and the first that does not, lie within a
+// tolerance (keys: twice the error of the fp32 score, below 1e-6, and the
+// bits that the index took) is ranked again in fp64. Without a bias the
+// logits themselves rank like the scores; bf16 logits leave 16 bits free, which
+// hold the whole index, so that no two keys are equal.
 
 struct RouteParams {
     const void* logits;   // [T, E]
@@ -86,25 +93,78 @@ __device__ __forceinline__ float from_ordered_bits(uint32_t u) {
     return __uint_as_float((u & 0x80000000u) ? (u ^ 0x80000000u) : ~u);
 }
 
-template <typename Key>
-__device__ __forceinline__ bool near_keys(Key a, Key b) {
-    // equal infinities differ by NaN: not near, their order goes by the index
-    const Key d = a - b;
-    const Key m = fmax(static_cast<Key>(1), fmax(fabs(a), fabs(b)));
-    return fabs(d) <= static_cast<Key>(ROUTE_TOL) * m;
+// Bits of a key that hold its register's index.
+template <int V>
+__host__ __device__ constexpr int route_index_bits() {
+    int b = 0;
+    while ((1 << b) < V) ++b;
+    return b;
+}
+// Relative difference (to 1, for keys below 1) under which two fp32 keys may be in the wrong order.
+template <int V>
+__device__ constexpr float route_tolerance() { return 4e-6f + 2.4e-7f * (1 << route_index_bits<V>()); }
+
+// A sorting network (Knuth, The Art of Computer Programming 3, algorithm 5.2.2M:
+// merge exchange) for n keys as a list of compare-exchange pairs.
+struct SortNetwork {
+    int a[192], b[192], n;
+};
+__host__ __device__ constexpr SortNetwork sort_network(int n) {
+    SortNetwork net{};
+    int t = 0;
+    while ((1 << t) < n) ++t;
+    for (int p = t > 0 ? 1 << (t - 1) : 0; p > 0; p /= 2) {
+        int q = 1 << (t - 1), r = 0, d = p;
+        while (true) {
+            for (int i = 0; i + d < n; ++i)
+                if ((i & p) == r) {
+                    net.a[net.n] = i;
+                    net.b[net.n] = i + d;
+                    ++net.n;
+                }
+            if (q == p) break;
+            d = q - p;
+            q /= 2;
+            r = p;
+        }
+    }
+    return net;
 }
 
-// The groups that stay, as a bit mask over groups. `near` is set when two
-// groups' scores lie within the tolerance of each other.
-template <int V, typename Key>
-__device__ __forceinline__ uint32_t route_groups(const RouteParams& p, const Key (&key)[V], int lane, bool& near) {
-    const int size = p.experts / p.groups;
-    const int run = size / V;  // lanes of a group, when its experts fill whole lanes
-    Key score = static_cast<Key>(-INFINITY);  // lane g: the score of group g
-    if (size % V == 0 && (run & (run - 1)) == 0) {
-        Key b1 = static_cast<Key>(-INFINITY), b2 = b1;
+// The lane's keys in falling order.
+template <int V>
+__device__ __forceinline__ void sort_keys(uint32_t (&key)[V]) {
+    constexpr SortNetwork net = sort_network(V);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
+    for (int i = 0; i < net.n; ++i) {
+        const uint32_t hi = max(key[net.a[i]], key[net.b[i]]), lo = min(key[net.a[i]], key[net.b[i]]);
+        key[net.a[i]] = hi;
+        key[net.b[i]] = lo;
+    }
+}
+
+// The groups that stay, as a bit mask over groups: those of the top_groups best
+// scores (lane g holds the score of group g).
+template <typename Key>
+__device__ __forceinline__ uint32_t route_rank_groups(const RouteParams& p, Key score, int lane) {
+    int rank = 0;
+    for (int h = 0; h < p.groups; ++h) {
+        const Key other = __shfl_sync(0xffffffffu, score, h);
+        rank += (other > score || (other == score && h < lane)) ? 1 : 0;
+    }
+    return __ballot_sync(0xffffffffu, lane < p.groups && rank < p.top_groups);
+}
+
+// Score of group `lane` (in lanes below p.groups) from keys in registers in any order.
+template <int V, typename Key>
+__device__ __forceinline__ Key route_group_score(const RouteParams& p, const Key (&key)[V], int lane) {
+    const int size = p.experts / p.groups;
+    const int run = size / V;
+    if (size % V == 0 && (run & (run - 1)) == 0) {
+        // a group is a run of lanes
+        Key b1 = key[0], b2 = static_cast<Key>(-INFINITY);
+#pragma unroll
+        for (int i = 1; i < V; ++i) {
             b2 = fmax(b2, fmin(b1, key[i]));
             b1 = fmax(b1, key[i]);
         }
@@ -113,38 +173,28 @@ __device__ __forceinline__ uint32_t route_groups(const RouteParams& p, const Key
             b2 = fmax(fmin(b1, c1), fmax(b2, c2));
             b1 = fmax(b1, c1);
         }
-        const Key s = rank_key(p.group_top == 2 ? b1 + b2 : b1);
-        const Key mine = __shfl_sync(0xffffffffu, s, (lane * run) & 31);
-        if (lane < p.groups) score = mine;
-    } else {
-        for (int g = 0; g < p.groups; ++g) {
-            Key b1 = static_cast<Key>(-INFINITY), b2 = b1;
+        return __shfl_sync(0xffffffffu, rank_key(p.group_top == 2 ? b1 + b2 : b1), (lane * run) & 31);
+    }
+    Key score = static_cast<Key>(-INFINITY);
+    for (int g = 0; g < p.groups; ++g) {
+        Key b1 = static_cast<Key>(-INFINITY), b2 = b1;
 #pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = lane * V + i;
-                if (e >= g * size && e < (g + 1) * size) {
-                    b2 = fmax(b2, fmin(b1, key[i]));
-                    b1 = fmax(b1, key[i]);
-                }
+        for (int i = 0; i < V; ++i) {
+            const int e = lane * V + i;
+            if (e >= g * size && e < (g + 1) * size) {
+                b2 = fmax(b2, fmin(b1, key[i]));
+                b1 = fmax(b1, key[i]);
             }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const Key c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
-                b2 = fmax(fmin(b1, c1), fmax(b2, c2));
-                b1 = fmax(b1, c1);
-            }
-            if (lane == g) score = rank_key(p.group_top == 2 ? b1 + b2 : b1);
         }
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const Key c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+            b2 = fmax(fmin(b1, c1), fmax(b2, c2));
+            b1 = fmax(b1, c1);
+        }
+        if (lane == g) score = rank_key(p.group_top == 2 ? b1 + b2 : b1);
     }
-    int rank = 0;
-    near = false;
-    for (int h = 0; h < p.groups; ++h) {
-        const Key other = __shfl_sync(0xffffffffu, score, h);
-        rank += (other > score || (other == score && h < lane)) ? 1 : 0;
-        near |= h != lane && lane < p.groups && near_keys(other, score);
-    }
-    near = __any_sync(0xffffffffu, near) != 0;
-    return __ballot_sync(0xffffffffu, lane < p.groups && rank < p.top_groups);
+    return score;
 }
 
 // Experts of this lane that may be chosen, as a bit mask over its registers.
@@ -160,57 +210,93 @@ __device__ __forceinline__ uint32_t route_alive(const RouteParams& p, uint32_t k
     return alive;
 }
 
-// Scores of this lane's experts in fp64 (the second look at close choices).
+// Unrolling of the fp64 loops: whole while the arrays stay in registers.
+template <int V>
+__host__ __device__ constexpr int route_unroll64() { return V <= 8 ? V : 1; }
+
+// Maximum and 1 / sum of a softmax row in fp64 (0 where every logit is -inf).
 template <int V, bool F32>
-__device__ __noinline__ void route_scores64(const RouteParams& p, size_t row, int lane, double (&s)[V]) {
-    double m = -INFINITY;
-    for (int i = 0; i < V; ++i) {
-        const int e = lane * V + i;
-        s[i] = e < p.experts ? static_cast<double>(load_logit<F32>(p.logits, row + e)) : -INFINITY;
-        m = fmax(m, s[i]);
-    }
-    if (!p.softmax) {
-        for (int i = 0; i < V; ++i) s[i] = 1.0 / (1.0 + exp(-s[i]));
-        return;
-    }
-    for (int o = 16; o > 0; o >>= 1) m = fmax(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (m == -INFINITY) m = 0.0;
+__device__ __forceinline__ void route_softmax64(const RouteParams& p, size_t row, int lane, double& top, double& inv) {
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        if (lane * V + i < p.experts) m = fmaxf(m, load_logit<F32>(p.logits, row + lane * V + i));
+    m = warp_max(m);
+    top = m == -INFINITY ? 0.0 : static_cast<double>(m);
     double sum = 0.0;
-    for (int i = 0; i < V; ++i) {
-        s[i] = exp(s[i] - m);
-        sum += s[i];
-    }
+#pragma unroll route_unroll64<V>()
+    for (int i = 0; i < V; ++i)
+        if (lane * V + i < p.experts) sum += exp(static_cast<double>(load_logit<F32>(p.logits, row + lane * V + i)) - top);
+#pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const double inv = sum == 0.0 ? 0.0 : 1.0 / sum;
-    for (int i = 0; i < V; ++i) s[i] *= inv;
+    inv = sum == 0.0 ? 0.0 : 1.0 / sum;
 }
 
-// The choice again with fp64 keys: lane j < k returns its expert.
+__device__ __forceinline__ double route_score64(const RouteParams& p, float x, double top, double inv) {
+    const double v = static_cast<double>(x);
+    return p.softmax ? exp(v - top) * inv : 1.0 / (1.0 + exp(-v));
+}
+
+// Candidate `expert` of every lane below n, ranked by fp64 keys: lane j < n
+// returns the j-th. Candidates are in falling order of their fp32 keys, and all
+// experts that these leave undecided are among them.
+template <int V, bool F32>
+__device__ __noinline__ int route_order64(const RouteParams& p, size_t row, int lane, int expert, int n) {
+    double top = 0.0, inv = 0.0;
+    if (p.bias != nullptr && p.softmax) route_softmax64<V, F32>(p, row, lane, top, inv);
+    double key = -INFINITY;
+    if (lane < n) {
+        const float x = load_logit<F32>(p.logits, row + expert);
+        // without a bias the experts are ranked by their logits
+        key = rank_key(p.bias == nullptr ? static_cast<double>(x)
+                                         : route_score64(p, x, top, inv) + static_cast<double>(__ldg(p.bias + expert)));
+    }
+    int rank = 0;
+    for (int l = 0; l < n; ++l) {
+        const double k = __shfl_sync(0xffffffffu, key, l);
+        const int e = __shfl_sync(0xffffffffu, expert, l);
+        rank += (k > key || (k == key && e < expert)) ? 1 : 0;
+    }
+    int mine = 0;
+    for (int l = 0; l < n; ++l) {
+        const int r = __shfl_sync(0xffffffffu, rank, l), e = __shfl_sync(0xffffffffu, expert, l);
+        if (r == lane) mine = e;
+    }
+    return mine;
+}
+
+// The whole choice again with fp64 keys (groups too close, or more candidates
+// than lanes): lane j < k returns its expert.
 template <int V, bool F32>
 __device__ __noinline__ int route_choose64(const RouteParams& p, size_t row, int lane) {
+    double top = 0.0, inv = 0.0;
+    if (p.softmax) route_softmax64<V, F32>(p, row, lane, top, inv);
     double s[V], key[V];
-    route_scores64<V, F32>(p, row, lane, s);
+#pragma unroll route_unroll64<V>()
     for (int i = 0; i < V; ++i) {
         const int e = lane * V + i;
-        if (p.bias != nullptr && e < p.experts) s[i] += static_cast<double>(__ldg(p.bias + e));
-        s[i] = e < p.experts ? rank_key(s[i]) : -INFINITY;
-        // without a bias the experts are ranked by their logits
-        key[i] = s[i];
-        if (p.bias == nullptr && e < p.experts) key[i] = rank_key(static_cast<double>(load_logit<F32>(p.logits, row + e)));
+        s[i] = key[i] = -INFINITY;
+        if (e < p.experts) {
+            const float x = load_logit<F32>(p.logits, row + e);
+            s[i] = rank_key(route_score64(p, x, top, inv) + (p.bias != nullptr ? static_cast<double>(__ldg(p.bias + e)) : 0.0));
+            // without a bias the experts are ranked by their logits
+            key[i] = p.bias != nullptr ? s[i] : rank_key(static_cast<double>(x));
+        }
     }
     uint32_t kept = 0;
-    bool near;
-    if (p.top_groups < p.groups) kept = route_groups<V, double>(p, s, lane, near);
+    if (p.top_groups < p.groups) kept = route_rank_groups(p, route_group_score<V, double>(p, s, lane), lane);
     uint32_t alive = route_alive<V>(p, kept, lane);
     int mine = 0;
     for (int j = 0; j < p.k; ++j) {
         double best = -INFINITY;
         int e = MOE_MAX_EXPERTS;
+#pragma unroll route_unroll64<V>()
         for (int i = 0; i < V; ++i)
             if (((alive >> i) & 1u) && (e == MOE_MAX_EXPERTS || key[i] > best)) {
                 best = key[i];
                 e = lane * V + i;
             }
+#pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const double b = __shfl_xor_sync(0xffffffffu, best, o);
             const int f = __shfl_xor_sync(0xffffffffu, e, o);
@@ -227,105 +313,217 @@ __device__ __noinline__ int route_choose64(const RouteParams& p, size_t row, int
 
 constexpr int ROUTE_THREADS = 256;
 
+// A lane's V logits of one row: 16-byte loads when the rows allow (`vec`).
 template <int V, bool F32>
-__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_kernel(const RouteParams p) {
-    griddep_launch_dependents();
-    griddep_wait();
-    const int lane = static_cast<int>(threadIdx.x & 31u);
-    const int t = static_cast<int>((static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5);
-    if (t >= p.tokens) return;  // whole warps
-    const size_t row = static_cast<size_t>(t) * p.experts;
-    float x[V];
-    float top = -INFINITY;
+__device__ __forceinline__ void load_logits(const RouteParams& p, size_t row, int lane, bool vec, float (&x)[V]) {
+    constexpr int kPer = F32 ? 4 : 8;  // values in 16 bytes
+    if (V % kPer == 0 && vec) {
+        if (lane * V >= p.experts) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) x[i] = -INFINITY;
+            return;
+        }
+        const char* src = static_cast<const char*>(p.logits) + (row + lane * V) * (F32 ? 4 : 2);
+#pragma unroll
+        for (int i = 0; i < V / kPer; ++i) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4*>(src) + i);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (F32) {
+                    x[4 * i + j] = __uint_as_float(w[j]);
+                } else {
+                    x[(8 * i + 2 * j) % V] = __uint_as_float(w[j] << 16);
+                    x[(8 * i + 2 * j + 1) % V] = __uint_as_float(w[j] & 0xFFFF0000u);
+                }
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = lane * V + i;
         x[i] = e < p.experts ? load_logit<F32>(p.logits, row + e) : -INFINITY;
-        top = fmaxf(top, x[i]);
     }
-    // softmax: the row's maximum (0 where every logit is -inf) and 1 / sum (0 then)
-    float inv = 1.f;
-    if (p.softmax) {
-        top = warp_max(top);
-        if (top == -INFINITY) top = 0.f;
-        float sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) sum += lane * V + i < p.experts ? expf(x[i] - top) : 0.f;
-        sum = warp_sum(sum);
-        inv = sum == 0.f ? 0.f : 1.f / sum;
-    }
-    // Keys: scores plus bias, or without a bias the logits, which rank alike.
-    // The groups' scores need the scores themselves when they are sums.
-    const bool grouped = p.top_groups < p.groups;
+}
+
+template <int V, bool F32>
+__global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 3 : 1) moe_route_kernel(const RouteParams p) {
+    constexpr uint32_t kIndexMask = (1u << route_index_bits<V>()) - 1u;
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = static_cast<int>(threadIdx.x & 31u);
+    const int warps = static_cast<int>(gridDim.x * (ROUTE_THREADS / 32));
     const bool by_score = p.bias != nullptr;
-    float key[V];
-    uint32_t kept = 0;
-    bool close = false;
-    if (by_score || (grouped && p.group_top == 2)) {
-        float s[V];
+    const bool grouped = p.top_groups < p.groups;
+    // the groups' scores need the scores themselves when they are sums
+    const bool need_scores = by_score || (grouped && p.group_top == 2);
+    // bf16 logits ranked as they are: the whole index fits below them
+    const bool whole_index = !F32 && !by_score;
+    const int size = p.experts / p.groups;
+    const int run = size / V;  // lanes of a group, when its experts fill whole lanes
+    const bool runs = size % V == 0 && (run & (run - 1)) == 0;
+    const int my_group = runs ? min(lane / run, 31) : 0;
+    const bool partial = 32 * V != p.experts;  // lanes or registers without an expert
+    const bool vec = p.experts % V == 0 && (reinterpret_cast<uintptr_t>(p.logits) & 15) == 0 &&
+                     (static_cast<size_t>(p.experts) * (F32 ? 4 : 2)) % 16 == 0;
+    float bias[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = lane * V + i;
-            const float ex = __expf(p.softmax ? x[i] - top : -x[i]);
-            float v = p.softmax ? ex * inv : __fdividef(1.f, 1.f + ex);
-            // (1 + ex infinite or past __fdividef's range: the score is 0)
-            if (!p.softmax && x[i] < -80.f) v = 0.f;
-            if (by_score && e < p.experts) v += __ldg(p.bias + e);
-            s[i] = e < p.experts ? rank_key(v) : -INFINITY;
-            key[i] = by_score ? s[i] : rank_key(x[i]);
+    for (int i = 0; i < V; ++i) bias[i] = by_score && lane * V + i < p.experts ? __ldg(p.bias + lane * V + i) : 0.f;
+
+    for (int t = static_cast<int>(blockIdx.x) * (ROUTE_THREADS / 32) + static_cast<int>(threadIdx.x >> 5); t < p.tokens;
+         t += warps) {
+        const size_t row = static_cast<size_t>(t) * p.experts;
+        float x[V];
+        load_logits<V, F32>(p, row, lane, vec, x);
+        // softmax: the row's maximum (0 where every logit is -inf) and 1 / sum (0 then)
+        float top = 0.f, inv = 1.f;
+        if (p.softmax) {
+            top = x[0];
+#pragma unroll
+            for (int i = 1; i < V; ++i) top = fmaxf(top, x[i]);
+            top = warp_max(top);
+            if (top == -INFINITY) top = 0.f;
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += lane * V + i < p.experts ? expf(x[i] - top) : 0.f;
+            sum = warp_sum(sum);
+            inv = sum == 0.f ? 0.f : 1.f / sum;
         }
-        if (grouped) kept = route_groups<V, float>(p, s, lane, close);
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = rank_key(x[i]);
-        bool near;  // the groups' best logits are exact
-        if (grouped) kept = route_groups<V, float>(p, key, lane, near);
-    }
-    int mine = 0;
-    if (!close) {
-        uint32_t alive = route_alive<V>(p, kept, lane);
-        uint32_t best = 0, before = 0;
-        int at = 0;
-        auto rescan = [&]() {
-            best = 0;
+        // scores plus bias in fp32
+        float s[V];
+        if (need_scores) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const uint32_t u = (alive >> i) & 1u ? ordered_bits(key[i]) : 0u;
-                if (u > best) {
-                    best = u;
-                    at = i;
+                if (p.softmax) {
+                    s[i] = fmaf(__expf(x[i] - top), inv, bias[i]);
+                } else {
+                    float r;  // (an infinite 1 + exp gives 0)
+                    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + __expf(-x[i])));
+                    s[i] = r + bias[i];
                 }
             }
-        };
-        rescan();
-        // one round more than k where the last choice may be a close one
-        const int rounds = p.k + (by_score ? 1 : 0);
-        for (int j = 0; j < rounds; ++j) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, best);
-            if (m == 0) break;  // nothing left (k is every expert there is)
-            if (by_score && j > 0) close |= near_keys(from_ordered_bits(before), from_ordered_bits(m));
-            before = m;
-            const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, best == m))) - 1;
-            const int e = __shfl_sync(0xffffffffu, lane * V + at, src);
-            if (lane == j) mine = e;
-            if (lane == src) {
-                alive &= ~(1u << at);
-                rescan();
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[i] = x[i];
+        }
+        // the keys (fmaxf: a NaN ranks as -inf)
+        uint32_t key[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            s[i] = fmaxf(s[i], -INFINITY);
+            const uint32_t u = ordered_bits((by_score ? s[i] : fmaxf(x[i], -INFINITY)) + 0.f);
+            key[i] = whole_index ? (u & ~1023u) | (1023u - static_cast<uint32_t>(lane * V + i))
+                                 : (u & ~kIndexMask) | static_cast<uint32_t>(V - 1 - i);
+        }
+        if (partial) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (lane * V + i >= p.experts) {
+                    s[i] = -INFINITY;
+                    key[i] = 0u;
+                }
+        }
+        bool close = false;
+        if (grouped) {
+            float score;
+            if (runs && by_score) {
+                // each lane's two best, from its sorted keys
+                sort_keys<V>(key);
+                float b1 = key[0] ? from_ordered_bits(key[0] & ~kIndexMask) : -INFINITY, b2 = -INFINITY;
+                if (V > 1 && key[V > 1 ? 1 : 0]) b2 = from_ordered_bits(key[V > 1 ? 1 : 0] & ~kIndexMask);
+                for (int o = 1; o < run; o <<= 1) {
+                    const float c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
+                    b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
+                    b1 = fmaxf(b1, c1);
+                }
+                score = __shfl_sync(0xffffffffu, rank_key(p.group_top == 2 ? b1 + b2 : b1), (lane * run) & 31);
+            } else {
+                score = route_group_score<V, float>(p, s, lane);
+            }
+            const uint32_t kept = route_rank_groups(p, score, lane);
+            if (need_scores) {
+                // the worst group that stays against the best that does not (the best
+                // logits of groups are exact, sums and biased scores are not)
+                const uint32_t u = ordered_bits(score);
+                const bool stays = (kept >> lane) & 1u;
+                const uint32_t lo = __reduce_min_sync(0xffffffffu, stays ? u : 0xffffffffu);
+                const uint32_t hi = __reduce_max_sync(0xffffffffu, !stays && lane < p.groups ? u : 0u);
+                const float least = from_ordered_bits(lo), best_out = from_ordered_bits(hi);
+                // (a difference of infinities is no number, and not close: their order goes by the index)
+                close = least - best_out <= 2.f * route_tolerance<V>() * fmaxf(1.f, fabsf(least));
+            }
+            if (runs) {
+                if (!((kept >> my_group) & 1u)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) key[i] = 0u;
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < V; ++i)
+                    if (!((kept >> min((lane * V + i) / size, 31)) & 1u)) key[i] = 0u;
             }
         }
-    }
-    if (close) mine = route_choose64<V, F32>(p, row, lane);
-    // weights, from the chosen experts' logits
-    float s = 0.f;
-    if (lane < p.k) {
-        const float v = load_logit<F32>(p.logits, row + mine);
-        s = p.softmax ? expf(v - top) * inv : 1.f / (1.f + expf(-v));
-    }
-    float w = p.scale * s;
-    if (p.renorm) w /= warp_sum(lane < p.k ? s : 0.f) + ROUTE_EPS;
-    if (lane < p.k) {
-        p.ids[static_cast<size_t>(t) * p.k + lane] = mine;
-        p.weights[static_cast<size_t>(t) * p.k + lane] = w;
+        int mine = 0;
+        if (close) {
+            mine = route_choose64<V, F32>(p, row, lane);
+        } else {
+            if (!(grouped && runs && by_score)) sort_keys<V>(key);
+            uint32_t my_key = 0, last = 0;
+            int my_src = 0;
+            // the j-th largest key, kept by lane j (0: nothing is left)
+            auto take = [&](int j) {
+                last = __reduce_max_sync(0xffffffffu, key[0]);
+                const int src = __ffs(static_cast<int>(__ballot_sync(0xffffffffu, key[0] == last))) - 1;
+                if (lane == j) {
+                    my_key = last;
+                    my_src = src;
+                }
+                const bool up = lane == src;
+#pragma unroll
+                for (int i = 0; i + 1 < V; ++i) key[i] = up ? key[i + 1] : key[i];
+                key[V - 1] = up ? 0u : key[V - 1];
+            };
+            // one more than k: the last choice may be a close one
+            for (int j = 0; j <= p.k; ++j) take(j);
+            // logits: equal but for the index's bits; scores: within the tolerance
+            auto near = [&](uint32_t above, uint32_t below) {
+                if (whole_index || below == 0u) return false;
+                if (!by_score) return ((above ^ below) & ~kIndexMask) == 0u;
+                const float a = from_ordered_bits(above & ~kIndexMask), b = from_ordered_bits(below & ~kIndexMask);
+                return a - b <= route_tolerance<V>() * fmaxf(1.f, fmaxf(fabsf(a), fabsf(b)));
+            };
+            uint32_t next = __shfl_down_sync(0xffffffffu, my_key, 1);
+            if (lane == p.k - 1) next = last;
+            const bool redo = __any_sync(0xffffffffu, lane < p.k && near(my_key, next)) != 0;
+            // further candidates while they are close to the one before
+            int n = p.k + 1;
+            if (redo) {
+                uint32_t above = __shfl_sync(0xffffffffu, my_key, p.k - 1);
+                while (n < 32 && near(above, last)) {
+                    above = last;
+                    take(n++);
+                }
+            }
+            mine = whole_index ? 1023 - static_cast<int>(my_key & 1023u)
+                               : my_src * V + V - 1 - static_cast<int>(my_key & kIndexMask);
+            if (redo) {
+                if (n >= 32) mine = route_choose64<V, F32>(p, row, lane);
+                else mine = route_order64<V, F32>(p, row, lane, mine, __popc(__ballot_sync(0xffffffffu, lane < n && my_key != 0u)));
+            }
+        }
+        // weights, from the chosen experts' logits
+        float w = 0.f;
+        if (lane < p.k) {
+            const float v = load_logit<F32>(p.logits, row + mine);
+            w = p.softmax ? expf(v - top) * inv : 1.f / (1.f + expf(-v));
+        }
+        float out = p.scale * w;
+        if (p.renorm) out /= warp_sum(w) + ROUTE_EPS;
+        if (lane < p.k) {
+            p.ids[static_cast<size_t>(t) * p.k + lane] = mine;
+            p.weights[static_cast<size_t>(t) * p.k + lane] = out;
+        }
     }
 }
 

@@ -97,14 +97,19 @@ def test_route_ties_go_to_the_lowest_index():
 
 
 @pytest.mark.parametrize("n,top,gt", [(1, 1, 1), (8, 4, 2), (8, 4, 1)])
-def test_route_choices_closer_than_fp32(n, top, gt):
-    """Keys that differ by 2^-26: the bias makes up all but that of the score's
-    difference, so fp32 keys tie or swap, and the 64-bit order must come out."""
-    T, E, k = 64, 64, 8
+@pytest.mark.parametrize("E,tied", [(64, 64), (64, 2), (64, 5), (256, 3), (512, 4), (60, 2)])
+def test_route_choices_closer_than_fp32(n, top, gt, E, tied):
+    """Keys that differ by 2^-26 in runs of `tied` experts: the bias makes up all
+    but that of the score's difference, so fp32 keys tie or swap, and the 64-bit
+    order must come out."""
+    if E % n:
+        n, top = 4, 2
+    T, k = 64, 8
     g = torch.Generator().manual_seed(5)
     x = torch.randn((T, E), generator=g).double()
     base = torch.sigmoid(x[0].float().double())
-    want = 0.7 + 2.0 ** -26 * torch.randperm(E, generator=g).double()
+    step = torch.randperm(E, generator=g)
+    want = 0.7 + 2.0 ** -26 * step.double() + 1e-3 * (step // tied).double()
     bias = (want - base).float()
     x = x[:1].float().expand(T, E).contiguous()
     x[1:] += 1e-7 * torch.randn((T - 1, E), generator=g)
@@ -138,6 +143,26 @@ def test_route_rows_with_nothing_or_with_what_is_not_finite():
         assert w2[0].tolist() == [0, 0, 0, 0]
         assert torch.isfinite(w2[5]).all()
         assert not torch.isnan(w2[3]).any()   # the NaN expert ranks last and is not chosen
+
+
+def test_route_many_tokens():
+    """More tokens than warps at once, among them the choices that 16384 random
+    tokens leave undecided in fp32."""
+    T, E, k = 16384, 256, 8
+    g = torch.Generator().manual_seed(77)
+    x = 1.5 * torch.randn((T, E), generator=g)
+    b = 0.05 * torch.randn((E,), generator=g)
+    ids, w = dg.moe_route(x.cuda(), k, bias=b.cuda(), score="sigmoid", n_groups=8, top_groups=4)
+    s = torch.sigmoid(x.double())
+    key = s + b.double()
+    best = key.view(T, 8, 32).sort(dim=2, descending=True).values[:, :, :2].sum(2)
+    kept = best.sort(dim=1, descending=True, stable=True).indices[:, :4]
+    mask = torch.zeros((T, 8), dtype=torch.bool).scatter_(1, kept, True).repeat_interleave(32, dim=1)
+    want = key.masked_fill(~mask, -np.inf).sort(dim=1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.cpu().long(), want)
+    ref = s.gather(1, want)
+    ref = (ref / ref.sum(1, keepdim=True)).numpy()
+    assert np.all(np.abs(f64(w) - ref) <= weight_bound(f64(x[:1]), k, "sigmoid") * ref)
 
 
 @pytest.mark.parametrize("case", ROUTE)
