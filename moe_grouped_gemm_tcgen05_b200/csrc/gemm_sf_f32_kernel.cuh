@@ -215,7 +215,7 @@ struct SfF32Config {
     static constexpr int STG_BYTES = EW * 32 * STG_ROW;
     // scales of four K-blocks per slot: [4][128 rows] (times B's, when that is one
     // per 128 columns), and with ROWB [4][BN columns]
-    static constexpr int SF_SLOTS = 2;
+    static constexpr int SF_SLOTS = ROWB ? 4 : 2;
     static constexpr int SF_SLOT_FLOATS = 4 * BM + (ROWB ? 4 * BN : 0);
     static constexpr int SF_BYTES = SF_SLOTS * SF_SLOT_FLOATS * 4;
     static constexpr int SCHED_BYTES = SCHED_INTS * 4;
@@ -585,6 +585,16 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
              t += units) {
             const int mloc = c.m_blk * BM * CG + my_rows + 32 * q + static_cast<int>(lane);
             const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
+            if constexpr (EPI == 1) {
+                // C's part of the tile on its way to L2, a K loop ahead of its use
+                const int col = c.n_blk * BN + grp * CW;
+                if (p.c != nullptr && mloc < p.rows) {
+                    const int size = p.out_f32 ? 4 : 2;
+                    const char* row = static_cast<const char*>(p.c) + (static_cast<size_t>(mloc) * p.n + col) * size;
+                    for (int b = 0; b < CW * size; b += 128)
+                        if (col + b / size < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + b));
+                }
+            }
             float acc[CW];
 #pragma unroll
             for (int i = 0; i < CW; ++i) acc[i] = 0.f;
@@ -596,8 +606,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 const float* sf = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 32 * q + lane;
                 [[maybe_unused]] const float* sfb_cols = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 4 * BM + grp * CW;
                 const int n = min(4, kb1 - kb);
-                // (not unrolled: the loop's code stays in the innermost instruction cache)
-#pragma unroll 1
+#pragma unroll 2
                 for (int i = 0; i < n; ++i) {
                     const float f = sf[i * BM];
                     if (!__all_sync(0xffffffffu, mbar_try_wait_addr(done0 + 8 * stage, par)) &&

@@ -348,7 +348,7 @@ __device__ __forceinline__ void load_logits(const RouteParams& p, size_t row, in
 }
 
 template <int V, bool F32>
-__global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 3 : 1) moe_route_kernel(const RouteParams p) {
+__global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kernel(const RouteParams p) {
     constexpr uint32_t kIndexMask = (1u << route_index_bits<V>()) - 1u;
     griddep_launch_dependents();
     griddep_wait();
@@ -845,6 +845,9 @@ __global__ void __launch_bounds__(DISPATCH_THREADS) moe_dispatch_fp8_kernel(cons
         const int word = static_cast<int>(i - static_cast<int64_t>(t) * p.kp);
         const int block = 4 * word + (lane >> 3);
         const bool there = block < p.kb;
+        // the token's rows, one per lane (k <= 32), loaded beside its values
+        int64_t my_row = p.row_of != nullptr ? -1 : t;
+        if (p.row_of != nullptr && lane < p.k) my_row = __ldg(p.row_of + static_cast<int64_t>(t) * p.k + lane);
         float v[16];
         if (there) {
             load16<IN_F32>(p.x, (static_cast<int64_t>(t) * p.kb + block) * 128 + 16 * (lane & 7), v);
@@ -882,7 +885,7 @@ __global__ void __launch_bounds__(DISPATCH_THREADS) moe_dispatch_fp8_kernel(cons
             packed |= __shfl_xor_sync(0xffffffffu, packed, 16);
         }
         for (int j = 0; j < p.k; ++j) {
-            const int64_t r = p.row_of != nullptr ? __ldg(p.row_of + static_cast<int64_t>(t) * p.k + j) : t;
+            const int64_t r = __shfl_sync(0xffffffffu, my_row, j);
             if (r < 0 || r >= p.rows) continue;  // the same in every lane
             if (there) p.q[(r * p.kb + block) * 8 + (lane & 7)] = codes;
             if constexpr (SF_F32) {
