@@ -167,7 +167,8 @@ DG_API dg_status dgb200_set_splits(int splits);
  * Test hook for the failure path (process-wide). wait_limit_ms bounds every
  * wait inside the GEMM kernels (0 restores the default, 2000 ms). mode 1 makes
  * CTA 0 of each GEMM launch withhold the arrive that publishes its first group
- * of scale words, so a wait runs out: that launch leaves its output incomplete, sets
+ * of scale words (the *_sf_f32 GEMMs: its first operand load), so a wait runs
+ * out: that launch leaves its output incomplete, sets
  * DG_DEVERR_TIMEOUT and returns; the CUDA context stays usable. mode 0 is
  * normal operation.
  */
@@ -434,7 +435,8 @@ DG_API dg_status quantize_fp8_1x128(const void* x, int x_f32, void* q, int32_t* 
  * takes both operands transposed and quantised along the tokens (sfb_gran_n =
  * 1), with an fp32 D that C accumulates into.
  * dgb200_set_block_n, _set_cta_group and _set_splits apply; a combination that
- * is not built returns DG_ERR_UNSUPPORTED.
+ * is not built (tiles are 128 columns wide; CTA pairs exist for the dense form)
+ * returns DG_ERR_UNSUPPORTED.
  */
 DG_API dg_status fp8_gemm_nt_sf_f32(const void* a, const float* sfa, const void* b, const float* sfb, int sfb_gran_n,
                                     const void* c, void* d, int M, int N, int K, int out_f32, void* stream);
@@ -466,7 +468,7 @@ DG_API dg_status m_grouped_fp8_gemm_nt_masked_sf_f32(const void* a, const float*
  * NaN key ranks below every number; a NaN or +inf logit makes the softmax
  * weights of its row NaN. Ids are always k different experts.
  * Limits: 1 <= k <= E <= 1024, k <= 32, n_groups <= 32 and a divisor of E,
- * k <= top_groups * E / n_groups. Capture safe.
+ * k <= top_groups * E / n_groups, T <= 2^30. Capture safe.
  */
 #define DG_SCORE_SOFTMAX 0
 #define DG_SCORE_SIGMOID 1
@@ -502,8 +504,8 @@ DG_API dg_status moe_route_backward(const void* logits, int logits_f32, const in
  * moe_rows_masked lays them out for m_grouped_fp8_gemm_nt_masked: expert e
  * owns rows e*max_m ... of [G, max_m]. Choices past max_m get row -1.
  *   masked_m  : device, int32 [G], min(counts, max_m)
- * Every output is written completely. Limits: k <= 32, G <= 1024, fewer than
- * 2^31 rows. One launch, no workspace, capture safe.
+ * Every output is written completely. Limits: k <= 32, G <= 1024, T*k <= 2^30,
+ * m_rows < 2^31 - 128, G*max_m < 2^30. One launch, no workspace, capture safe.
  */
 DG_API int64_t moe_rows_bound(int T, int k, int G);
 DG_API dg_status moe_rows_contiguous(const int32_t* ids, int32_t* row_of, int32_t* m_indices, int32_t* counts, int T,

@@ -236,7 +236,8 @@ dg_status setup_device(int dev, DeviceState& st) {
     void* status = nullptr;
     if (cudaGetSymbolAddress(&status, g_dg_device_status) != cudaSuccess) return DG_ERR_CUDA;
     st.status = static_cast<uint32_t*>(status);
-    return dg::setup_sf_f32(dev, st.sms);
+    const dg_status s = dg::setup_moe();
+    return s != DG_OK ? s : dg::setup_sf_f32(dev, st.sms);
 }
 
 // Set up device `dev`, which must be the current device. Allocates nothing.

@@ -39,6 +39,7 @@ const Entry kEntries[] = {
 constexpr int kNumEntries = sizeof(kEntries) / sizeof(kEntries[0]);
 
 struct Device {
+    bool ready = false;
     int units[kNumEntries] = {};                                // co-resident CTAs, or CTA pairs
     int clusters[kNumEntries][dg::MAX_CLUSTER_SPLITS + 1] = {};  // co-resident clusters of s CTAs (dense, single CTAs)
 };
@@ -210,6 +211,7 @@ namespace dg {
 
 dg_status setup_sf_f32(int device, int sms) {
     Device& dev = g_devices[device];
+    if (dev.ready) return DG_OK;
     for (int i = 0; i < kNumEntries; ++i) {
         const Entry& e = kEntries[i];
         if (cudaFuncSetAttribute(e.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, e.smem) != cudaSuccess)
@@ -229,6 +231,7 @@ dg_status setup_sf_f32(int device, int sms) {
             }
         }
     }
+    dev.ready = true;
     return DG_OK;
 }
 

@@ -33,6 +33,9 @@ bool host_log();                // DGB200_LOG
 // current device (gemm_sf_f32.cu); part of the device's set-up.
 dg_status setup_sf_f32(int device, int sms);
 
+// Kernel attributes of the calls around the experts' products (moe.cu).
+dg_status setup_moe();
+
 inline bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // A launch with programmatic stream serialization (unless switched off) and

@@ -66,7 +66,7 @@ bool flag(int v) { return v == 0 || v == 1; }
 // T tokens of E experts, k of them chosen.
 dg_status check_route_sizes(int T, int E, int k) {
     if (T <= 0 || E <= 0 || k <= 0 || k > E) return DG_ERR_INVALID_ARG;
-    if (E > dg::MOE_MAX_EXPERTS || k > dg::MOE_MAX_TOPK) return DG_ERR_UNSUPPORTED;
+    if (E > dg::MOE_MAX_EXPERTS || k > dg::MOE_MAX_TOPK || T > (1 << 30)) return DG_ERR_UNSUPPORTED;
     return DG_OK;
 }
 
@@ -86,9 +86,6 @@ dg_status rows_launch(dg::RowsParams& p, void* stream) {
     const dg_status s = dg::host_device(&dev);
     if (s != DG_OK) return s;
     const int smem = dg::rows_smem_bytes(p.groups);
-    if (smem > 48 * 1024 &&
-        cudaFuncSetAttribute(dg::moe_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return DG_ERR_CUDA;
     const unsigned ctas = p.n <= kRowsOneCta ? 1 : dg::ROWS_MAX_CLUSTER;
     cudaLaunchAttribute attr[2];
     cudaLaunchConfig_t cfg = dg::host_launch(ctas, dg::ROWS_THREADS, static_cast<size_t>(smem), stream, attr);
@@ -144,7 +141,22 @@ dg_status check_combine(const void* y, const int32_t* row_of, const float* w, co
     return DG_OK;
 }
 
+// One warp's step and an index past the end stay below 2^31.
+constexpr int64_t kMaxChoices = int64_t{1} << 30;
+
 }  // namespace
+
+namespace dg {
+
+dg_status setup_moe() {
+    // (one value for every call: calls on several threads share the attribute)
+    return cudaFuncSetAttribute(moe_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                rows_smem_bytes(MOE_MAX_EXPERTS)) == cudaSuccess
+               ? DG_OK
+               : DG_ERR_CUDA;
+}
+
+}  // namespace dg
 
 extern "C" {
 
@@ -206,7 +218,7 @@ dg_status moe_rows_contiguous(const int32_t* ids, int32_t* row_of, int32_t* m_in
     const dg_status s = check_rows(ids, row_of, m_indices, counts, T, k, G);
     if (s != DG_OK) return s;
     if (m_rows < row_bound(T, k, G)) return DG_ERR_INVALID_ARG;
-    if (m_rows > kMaxInt - 128) return DG_ERR_UNSUPPORTED;
+    if (m_rows > kMaxInt - 128 || static_cast<int64_t>(T) * k > kMaxChoices) return DG_ERR_UNSUPPORTED;
     dg::RowsParams p{ids, row_of, m_indices, counts, T * k, G, static_cast<int>(m_rows), 0};
     return rows_launch(p, stream);
 }
@@ -216,7 +228,8 @@ dg_status moe_rows_masked(const int32_t* ids, int32_t* row_of, int32_t* masked_m
     const dg_status s = check_rows(ids, row_of, masked_m, counts, T, k, G);
     if (s != DG_OK) return s;
     if (max_m <= 0) return DG_ERR_INVALID_ARG;
-    if (static_cast<int64_t>(G) * max_m + static_cast<int64_t>(T) * k > kMaxInt) return DG_ERR_UNSUPPORTED;
+    if (static_cast<int64_t>(T) * k > kMaxChoices || static_cast<int64_t>(G) * max_m > kMaxInt - kMaxChoices)
+        return DG_ERR_UNSUPPORTED;
     dg::RowsParams p{ids, row_of, masked_m, counts, T * k, G, 0, max_m};
     return rows_launch(p, stream);
 }

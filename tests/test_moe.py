@@ -104,7 +104,7 @@ def route_call(lib, **kw):
 @pytest.mark.parametrize("kw,status", [
     (dict(logits=None), 1), (dict(ids=None), 1), (dict(w=None), 1), (dict(f32=2), 1), (dict(renorm=-1), 1),
     (dict(T=0), 1), (dict(T=-3), 1), (dict(E=0), 1), (dict(k=0), 1), (dict(k=17), 1), (dict(E=1025), 3),
-    (dict(E=64, k=33), 3), (dict(score=2), 1), (dict(n=3), 1), (dict(n=0), 1), (dict(n=4, top=5), 1),
+    (dict(E=64, k=33), 3), (dict(T=(1 << 30) + 1), 3), (dict(score=2), 1), (dict(n=3), 1), (dict(n=0), 1), (dict(n=4, top=5), 1),
     (dict(n=4, top=0), 1), (dict(gt=3), 1), (dict(gt=0), 1), (dict(E=64, n=64), 3), (dict(n=8, top=1, k=3), 1),
     (dict(logits=VP(0x10002)), 2), (dict(f32=0, logits=VP(0x10001)), 2), (dict(bias=VP(0x10002)), 2),
     (dict(ids=VP(0x10002)), 2), (dict(w=VP(0x10001)), 2)])
@@ -137,6 +137,7 @@ def test_rows_refusals(lib):
     for kw in (dict(ids=None), dict(row=None), dict(m=None), dict(c=None), dict(T=0), dict(k=0), dict(G=0), dict(mm=0)):
         assert masked(**kw) == 1, kw
     assert masked(G=1024, mm=1 << 21) == 3 and masked(G=1025) == 3 and masked(T=1 << 30, k=32) == 3
+    assert masked(T=(1 << 30) + 1, k=1) == 3 and cont(T=(1 << 30) + 1, k=1, G=1, rows=(1 << 30) + 4096) == 3
     for T, k, G in ((1, 1, 1), (7, 3, 5), (4096, 8, 256), (0, 4, 4)):
         assert lib.moe_rows_bound(T, k, G) == (om.rows_bound(T, k, G) if T else 0)
 
