@@ -524,8 +524,8 @@ DG_API dg_status moe_rows_masked(const int32_t* ids, int32_t* row_of, int32_t* m
  *            (sf_f32 = 0), exactly as quantize_fp8_1x128 computes them, or
  *            fp32 [rows, H/128] (sf_f32 = 1), as quantize_fp8_1x128_sf_f32
  * Rows that no slot names (padding) are left as they were. Limits:
- * H % 128 == 0; x and q 16-byte aligned; values finite. Capture safe. The
- * gradient of the copies is moe_combine with weights = NULL.
+ * H % 128 == 0, T * H and rows * H < 2^40; x and q 16-byte aligned; values
+ * finite. Capture safe. The gradient of the copies is moe_combine with weights = NULL.
  */
 DG_API dg_status moe_dispatch_fp8(const void* x, int x_f32, const int32_t* row_of, void* q, void* sf, int sf_f32,
                                   int64_t rows, int T, int k, int H, void* stream);
@@ -554,7 +554,8 @@ DG_API dg_status quantize_fp8_1x128_sf_f32(const void* x, int x_f32, void* q, fl
  *   d_y[row_of[t, j]]  = weights[t, j] * d_out[t]      (bf16; other rows are left as they were)
  *   d_weights[t, j]    = <y[row_of[t, j]], d_out[t]>   (fp32; 0 for slots without a row)
  * row_of names different rows. Outputs must not overlap inputs. Limits:
- * H % 8 == 0, k <= 32; y, out, d_out, d_y 16-byte aligned. Capture safe.
+ * H % 8 == 0, k <= 32, T * H and rows * H < 2^40; y, out, d_out, d_y 16-byte
+ * aligned. Capture safe.
  */
 DG_API dg_status moe_combine(const void* y, const int32_t* row_of, const float* weights, void* out, int64_t rows, int T,
                              int k, int H, void* stream);

@@ -31,10 +31,11 @@ constexpr float ROUTE_EPS = 1e-20f;    // added to the sum that weights are divi
 // One warp per token, expert e = lane * V + i in register i of its lane, so a
 // group is a run of lanes whenever its size is V times a power of two.
 //
-// What bounds it: instructions. A token is ~1 KB of logits, and its choice ~500
-// warp instructions with the following representation (1824 with keys and
-// indices apart: 45 us for 16384 tokens of 256 experts, against the memory's
-// 2.6). A key is an unsigned integer that orders like the fp32 value, with
+// What bounds it: instructions. A token of 256 experts is 1 KB of fp32 logits, and
+// its choice ~870 warp instructions with the following representation (1824 with
+// keys and indices apart). 16384 such tokens take 30 us (45 with the indices
+// apart; the memory alone needs 2.7), 64 tokens 4.5 us, nearly all of it latency;
+// bf16 logits under softmax take 19 us. A key is an unsigned integer that orders like the fp32 value, with
 // the complement of the register's index in its lowest bits; a lane's keys are
 // sorted once, a round takes the largest first key of all lanes (one reduction),
 // and its lane moves up.
@@ -534,7 +535,8 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
 //   softmax       dx_i = s_i (ds_i - c),  c = sum_j ds_j s_j (scale * mean(g) * eps / S when renormalised)
 // The differences g_j - g_l keep the digits that g_j - mean(g) would cancel.
 // One warp per token; lane j < k holds choice j. Ids outside [0, E) count as
-// not chosen; an expert named twice gets both slots' gradients.
+// not chosen; an expert named twice gets both slots' gradients. 16384 tokens of
+// 256 experts take 7.0 us (33.6 MB: L2 holds them), 8191 of 32 in bf16 4.3 us.
 struct RouteBackwardParams {
     const void* logits;      // [T, E]
     const int32_t* ids;      // [T, k]
@@ -632,16 +634,24 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(const
 // the earlier experts' rows rounded up to whole 128-row blocks (contiguous
 // form), or e * max_m (masked form; ranks at or past max_m get row -1).
 //
-// One cluster of up to 8 CTAs does it in one launch, with no workspace: every
+// One cluster of up to 16 CTAs does it in one launch, with no workspace: every
 // warp owns a run of choices and a row of counters in shared memory, counts
 // it, the counters are turned into first rows by a scan over warps, CTAs
 // (through distributed shared memory) and experts, and the run is walked a
-// second time to hand the rows out. Ranks inside 32 choices come from
-// match_any. Bound by latency: the run of a warp is walked 32 choices a step.
+// second time to hand the rows out. Ranks inside 32 choices come from ballots
+// over the expert's bits (match_any takes a step per distinct expert: 65536
+// choices of 256 experts 16 us against 13, with 8 CTAs).
+//
+// Bound by the steps of 32 choices, each of which waits for the counters that the
+// last one left; four steps' loads and ballots overlap. 512 choices of 32 experts
+// take 6 us, 65536 of 256 experts 9.4 us, 524288 of them 31 us: next to the
+// dispatch that follows (99 us for those 65536, of 7168 values) a second launch
+// and a workspace would not pay.
 
 constexpr int ROWS_THREADS = 1024;
 constexpr int ROWS_WARPS = ROWS_THREADS / 32;
-constexpr int ROWS_MAX_CLUSTER = 8;
+constexpr int ROWS_MAX_CLUSTER = 16;  // CTAs of one GPC (148 SMs on 8 GPCs: one has 16 at least)
+constexpr int ROWS_BATCH = 4;         // steps of 32 choices that overlap
 
 struct RowsParams {
     const int32_t* ids;   // [n]; outside [0, G): no row
@@ -660,6 +670,43 @@ __device__ __forceinline__ int ld_cluster_s32(uint32_t addr) {
     int v;
     asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
     return v;
+}
+
+// Rows of the N * 32 choices from i0 on, in order; `next` holds the warp's next row of every expert.
+template <int N>
+__device__ __forceinline__ void rows_hand_out(const RowsParams& p, int* next, int i0, int end, int bits, int lane) {
+    int expert[N], row[N];
+    uint32_t same[N];  // lanes of the step whose choice is this lane's expert
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const int i = i0 + 32 * s + lane;
+        expert[s] = i < end ? __ldg(p.ids + i) : -1;
+        if (expert[s] < 0 || expert[s] >= p.groups) expert[s] = -1;  // (differs from every expert in bit `bits`)
+        same[s] = 0xffffffffu;
+    }
+    for (int b = 0; b <= bits; ++b) {
+#pragma unroll
+        for (int s = 0; s < N; ++s) {
+            const uint32_t mine = 0u - ((static_cast<uint32_t>(expert[s]) >> b) & 1u);  // the bit, in every lane's place
+            same[s] &= ~(__ballot_sync(0xffffffffu, mine) ^ mine);
+        }
+    }
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const int e = expert[s];
+        const int at = e >= 0 ? next[e] : 0;
+        __syncwarp();
+        row[s] = at + __popc(same[s] & ((1u << lane) - 1u));
+        if (e >= 0 && lane == 31 - __clz(static_cast<int>(same[s]))) next[e] = row[s] + 1;
+        __syncwarp();
+    }
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        const int i = i0 + 32 * s + lane, e = expert[s];
+        if (i >= end) continue;
+        const bool fits = e >= 0 && (p.max_m == 0 || row[s] - e * p.max_m < p.max_m);
+        p.row_of[i] = fits ? row[s] : -1;
+    }
 }
 
 __global__ void __launch_bounds__(ROWS_THREADS, 1) moe_rows_kernel(const RowsParams p) {
@@ -685,9 +732,13 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) moe_rows_kernel(const RowsPar
     const int begin = static_cast<int>(steps * me / warps * 32);
     const int end = static_cast<int>(min(static_cast<int64_t>(p.n), steps * (me + 1) / warps * 32));
     int* mine = hist + warp * G;
-    for (int i = begin + lane; i < end; i += 32) {
-        const int e = __ldg(p.ids + i);
-        if (e >= 0 && e < G) atomicAdd(mine + e, 1);  // whole numbers: any order gives the same count
+    for (int i0 = begin; i0 < end; i0 += 32 * ROWS_BATCH) {
+        int e[ROWS_BATCH];
+#pragma unroll
+        for (int b = 0; b < ROWS_BATCH; ++b) e[b] = i0 + 32 * b + lane < end ? __ldg(p.ids + i0 + 32 * b + lane) : -1;
+#pragma unroll
+        for (int b = 0; b < ROWS_BATCH; ++b)
+            if (e[b] >= 0 && e[b] < G) atomicAdd(mine + e[b], 1);  // whole numbers: any order gives the same count
     }
     __syncthreads();
 
@@ -745,21 +796,10 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) moe_rows_kernel(const RowsPar
         all_total[tid] = total;
     }
     __syncthreads();
-    for (int i0 = begin; i0 < end; i0 += 32) {
-        const int i = i0 + lane;
-        int e = i < end ? __ldg(p.ids + i) : -1;
-        if (e < 0 || e >= G) e = -1;
-        const uint32_t same = __match_any_sync(0xffffffffu, e);
-        const int at = e >= 0 ? mine[e] : 0;
-        __syncwarp();
-        const int row = at + __popc(same & ((1u << lane) - 1u));
-        if (e >= 0 && lane == 31 - __clz(static_cast<int>(same))) mine[e] = row + 1;
-        __syncwarp();
-        if (i < end) {
-            const bool fits = e >= 0 && (p.max_m == 0 || row - e * p.max_m < p.max_m);
-            p.row_of[i] = fits ? row : -1;
-        }
-    }
+    const int bits = 32 - __clz((G - 1) | 1);
+    int i0 = begin;
+    for (; i0 + 32 * ROWS_BATCH <= end; i0 += 32 * ROWS_BATCH) rows_hand_out<ROWS_BATCH>(p, mine, i0, end, bits, lane);
+    for (; i0 < end; i0 += 32) rows_hand_out<1>(p, mine, i0, end, bits, lane);
     if (p.max_m == 0) {
         // the expert of every row of every 128-row block; -1 on padding rows and past the last block
         const int blocks = (p.m_cap + 127) / 128;
@@ -795,6 +835,12 @@ __global__ void __launch_bounds__(ROWS_THREADS, 1) moe_rows_kernel(const RowsPar
 //
 // A warp handles four 128-value blocks of a token (one packed scale word):
 // lane l takes 16 values of block l / 8, whose amax is a maximum over 8 lanes.
+//
+// Bound by memory, its writes above all (80% of the bytes): 8192 tokens of 7168
+// bf16 values in 8 copies each move 602 MB in 99 us (6.1 TB/s), as a plain quantiser
+// (one copy) 4096 x 7168 take 18 us. A warp does one word and ends: eight CTAs per
+// SM that loop over words took 115 and 20.6 us (a warp's next load was issued
+// behind all its stores).
 
 constexpr int DISPATCH_THREADS = 256;
 
@@ -837,62 +883,59 @@ __global__ void __launch_bounds__(DISPATCH_THREADS) moe_dispatch_fp8_kernel(cons
     griddep_launch_dependents();
     griddep_wait();
     const int lane = static_cast<int>(threadIdx.x & 31u);
-    const int64_t warp0 = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t nwarps = (static_cast<int64_t>(gridDim.x) * blockDim.x) >> 5;
-    const int64_t words = static_cast<int64_t>(p.tokens) * p.kp;
-    for (int64_t i = warp0; i < words; i += nwarps) {
-        const int t = static_cast<int>(i / p.kp);
-        const int word = static_cast<int>(i - static_cast<int64_t>(t) * p.kp);
-        const int block = 4 * word + (lane >> 3);
-        const bool there = block < p.kb;
-        // the token's rows, one per lane (k <= 32), loaded beside its values
-        int64_t my_row = p.row_of != nullptr ? -1 : t;
-        if (p.row_of != nullptr && lane < p.k) my_row = __ldg(p.row_of + static_cast<int64_t>(t) * p.k + lane);
-        float v[16];
-        if (there) {
-            load16<IN_F32>(p.x, (static_cast<int64_t>(t) * p.kb + block) * 128 + 16 * (lane & 7), v);
-        } else {
+    const uint32_t i = blockIdx.x * (DISPATCH_THREADS / 32) + (threadIdx.x >> 5);  // (T * kp < 2^32 - 2^28)
+    const int t = static_cast<int>(i / static_cast<uint32_t>(p.kp));
+    const int word = static_cast<int>(i - static_cast<uint32_t>(t) * static_cast<uint32_t>(p.kp));
+    if (t >= p.tokens) return;
+    const int block = 4 * word + (lane >> 3);
+    const bool there = block < p.kb;
+    // the token's rows, one per lane (k <= 32), loaded beside its values
+    int64_t my_row = p.row_of != nullptr ? -1 : t;
+    if (p.row_of != nullptr && lane < p.k) my_row = __ldg(p.row_of + static_cast<int64_t>(t) * p.k + lane);
+    float v[16];
+    if (there) {
+        load16<IN_F32>(p.x, (static_cast<int64_t>(t) * p.kb + block) * 128 + 16 * (lane & 7), v);
+    } else {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = 0.f;
-        }
-        uint32_t m = __float_as_uint(1e-4f);
+        for (int j = 0; j < 16; ++j) v[j] = 0.f;
+    }
+    uint32_t m = __float_as_uint(1e-4f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    for (int j = 0; j < 16; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
 #pragma unroll
-        for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float scale, inv;
-        uint32_t byte = 0;
+    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+    float scale, inv;
+    uint32_t byte = 0;
+    if constexpr (SF_F32) {
+        scale = __uint_as_float(m) / 448.f;
+        inv = 448.f / __uint_as_float(m);
+    } else {
+        const int e = static_cast<int>((m >> 23) & 0xFFu) - 127 - 8 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+        byte = there ? static_cast<uint32_t>(127 + e) : 0u;
+        scale = 0.f;
+        inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    }
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        c[j] = e4m3x2_rn(v[4 * j + 1] * inv, v[4 * j] * inv) |
+               (e4m3x2_rn(v[4 * j + 3] * inv, v[4 * j + 2] * inv) << 16);
+    const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
+    // the four blocks' bytes meet in lane 0's word
+    uint32_t packed = 0;
+    if constexpr (!SF_F32) {
+        packed = byte << (8 * (lane >> 3));
+        packed |= __shfl_xor_sync(0xffffffffu, packed, 8);
+        packed |= __shfl_xor_sync(0xffffffffu, packed, 16);
+    }
+    for (int j = 0; j < p.k; ++j) {
+        const int64_t r = __shfl_sync(0xffffffffu, my_row, j);
+        if (r < 0 || r >= p.rows) continue;  // the same in every lane
+        if (there) p.q[(r * p.kb + block) * 8 + (lane & 7)] = codes;
         if constexpr (SF_F32) {
-            scale = __uint_as_float(m) / 448.f;
-            inv = 448.f / __uint_as_float(m);
+            if (there && (lane & 7) == 0) static_cast<float*>(p.sf)[r * p.kb + block] = scale;
         } else {
-            const int e = static_cast<int>((m >> 23) & 0xFFu) - 127 - 8 + ((m & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-            byte = there ? static_cast<uint32_t>(127 + e) : 0u;
-            scale = 0.f;
-            inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        }
-        uint32_t c[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-            c[j] = e4m3x2_rn(v[4 * j + 1] * inv, v[4 * j] * inv) |
-                   (e4m3x2_rn(v[4 * j + 3] * inv, v[4 * j + 2] * inv) << 16);
-        const uint4 codes = make_uint4(c[0], c[1], c[2], c[3]);
-        // the four blocks' bytes meet in lane 0's word
-        uint32_t packed = 0;
-        if constexpr (!SF_F32) {
-            packed = byte << (8 * (lane >> 3));
-            packed |= __shfl_xor_sync(0xffffffffu, packed, 8);
-            packed |= __shfl_xor_sync(0xffffffffu, packed, 16);
-        }
-        for (int j = 0; j < p.k; ++j) {
-            const int64_t r = __shfl_sync(0xffffffffu, my_row, j);
-            if (r < 0 || r >= p.rows) continue;  // the same in every lane
-            if (there) p.q[(r * p.kb + block) * 8 + (lane & 7)] = codes;
-            if constexpr (SF_F32) {
-                if (there && (lane & 7) == 0) static_cast<float*>(p.sf)[r * p.kb + block] = scale;
-            } else {
-                if (lane == 0) static_cast<uint32_t*>(p.sf)[r * p.kp + word] = packed;
-            }
+            if (lane == 0) static_cast<uint32_t*>(p.sf)[r * p.kp + word] = packed;
         }
     }
 }
@@ -902,7 +945,8 @@ __global__ void __launch_bounds__(DISPATCH_THREADS) moe_dispatch_fp8_kernel(cons
 // out[t] = sum_j w[t, j] y[row_of[t, j]], in fp32 in the order of j, rounded to
 // bf16 once. Slots without a row (outside [0, rows)) are not read and add
 // nothing. One thread per eight columns of a token, up to eight rows' loads in
-// flight.
+// flight. Bound by memory: 4096 tokens of 8 rows of 7168 values move 528 MB in
+// 83 us (6.4 TB/s; 87.5 with a grid that stays and loops).
 
 constexpr int COMBINE_THREADS = 256;
 constexpr int COMBINE_BATCH = 8;
@@ -939,47 +983,47 @@ __device__ __forceinline__ uint4 f32_to_bf16x8(const float (&v)[8]) {
 __global__ void __launch_bounds__(COMBINE_THREADS) moe_combine_kernel(const CombineParams p) {
     griddep_launch_dependents();
     griddep_wait();
-    const int64_t n = static_cast<int64_t>(p.tokens) * p.vecs;
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += stride) {
-        const int t = static_cast<int>(i / p.vecs);
-        const int c = static_cast<int>(i - static_cast<int64_t>(t) * p.vecs);
-        float acc[8];
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * COMBINE_THREADS + threadIdx.x;
+    if (i >= static_cast<int64_t>(p.tokens) * p.vecs) return;
+    const int t = static_cast<int>(i / p.vecs);
+    const int c = static_cast<int>(i - static_cast<int64_t>(t) * p.vecs);
+    float acc[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-        for (int j0 = 0; j0 < p.k; j0 += COMBINE_BATCH) {
-            uint4 u[COMBINE_BATCH];
-            float w[COMBINE_BATCH];
-            bool live[COMBINE_BATCH];
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int j0 = 0; j0 < p.k; j0 += COMBINE_BATCH) {
+        uint4 u[COMBINE_BATCH];
+        float w[COMBINE_BATCH];
+        bool live[COMBINE_BATCH];
 #pragma unroll
-            for (int j = 0; j < COMBINE_BATCH; ++j) {
-                live[j] = false;
-                if (j0 + j >= p.k) continue;
-                const int64_t at = static_cast<int64_t>(t) * p.k + j0 + j;
-                const int64_t r = __ldg(p.row_of + at);
-                live[j] = r >= 0 && r < p.rows;
-                if (!live[j]) continue;
-                w[j] = p.w != nullptr ? __ldg(p.w + at) : 1.f;
-                u[j] = __ldg(p.y + r * p.vecs + c);
-            }
-#pragma unroll
-            for (int j = 0; j < COMBINE_BATCH; ++j) {
-                if (!live[j]) continue;
-                float v[8];
-                bf16x8_to_f32(u[j], v);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], v[e], acc[e]);
-            }
+        for (int j = 0; j < COMBINE_BATCH; ++j) {
+            live[j] = false;
+            if (j0 + j >= p.k) continue;
+            const int64_t at = static_cast<int64_t>(t) * p.k + j0 + j;
+            const int64_t r = __ldg(p.row_of + at);
+            live[j] = r >= 0 && r < p.rows;
+            if (!live[j]) continue;
+            w[j] = p.w != nullptr ? __ldg(p.w + at) : 1.f;
+            u[j] = __ldg(p.y + r * p.vecs + c);
         }
-        p.out[i] = f32_to_bf16x8(acc);
+#pragma unroll
+        for (int j = 0; j < COMBINE_BATCH; ++j) {
+            if (!live[j]) continue;
+            float v[8];
+            bf16x8_to_f32(u[j], v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) acc[e] = fmaf(w[j], v[e], acc[e]);
+        }
     }
+    p.out[i] = f32_to_bf16x8(acc);
 }
 
 // Gradients of combine: d_y[row_of[t, j]] = w[t, j] d_out[t] (bf16) and
 // d_w[t, j] = <y[row_of[t, j]], d_out[t]> (fp32). Slots without a row get
 // d_w = 0; rows that no slot names are left as they were.
 // One CTA per token: its threads cover the columns and add up eight slots at a
-// time; the sums over threads go by warps and then in warp order.
+// time; the sums over threads go by warps and then in warp order. Bound by memory:
+// 4096 tokens of 8 rows of 7168 values move 998 MB in 161-164 us (6.1 TB/s);
+// d_w is why y is read at all, and both gradients come out of one pass over it.
 
 struct CombineBackwardParams {
     const uint4* y;         // [rows, H] bf16

@@ -158,6 +158,13 @@ def test_dispatch_and_quantiser_refusals(lib):
     assert quant(rows=1 << 31) == 3 and quant(x=VP(0x10004)) == 2 and quant(q=VP(0x10004)) == 2
 
 
+def test_token_matrices_past_the_limit_are_refused(lib):
+    T, H = 1 << 30, 1024   # 2^40 values
+    assert lib.moe_dispatch_fp8(GOOD, 0, GOOD, GOOD, GOOD, 1, 128, T, 2, H, None) == 3
+    assert lib.moe_combine(GOOD, GOOD, None, VP(0x20000), 128, T, 2, H, None) == 3
+    assert lib.moe_combine_backward(GOOD, GOOD, GOOD, GOOD, VP(0x20000), GOOD, 128, T, 2, H, None) == 3
+
+
 def test_combine_refusals(lib):
     def comb(y=GOOD, row=GOOD, w=None, out=VP(0x20000), rows=128, T=4, k=2, H=64):
         return lib.moe_combine(y, row, w, out, rows, T, k, H, None)

@@ -250,6 +250,31 @@ def test_rows(T, k, G, kind):
         assert np.array_equal(masked_m.cpu().numpy(), np.minimum(ref_counts, max_m))
 
 
+@pytest.mark.parametrize("T,k,G", [(9001, 8, 256), (16411, 5, 3), (2100, 32, 1024), (4100, 1, 1)])
+def test_rows_of_many_choices(T, k, G):
+    """Several whole batches of a warp's steps and a rest; ids outside the experts share low bits with those inside."""
+    r = np.random.default_rng(T)
+    ids = r.integers(0, G, (T, k)).astype(np.int64)
+    out = r.random((T, k)) < 0.1
+    ids[out] += r.choice([G, 1024, 2048, 2 ** 30, -G, -(2 ** 31)], size=int(out.sum()))
+    ids = ids.clip(-(2 ** 31), 2 ** 31 - 1).astype(np.int32)
+    row_of, m_idx, counts = dg.moe_rows_contiguous(torch.from_numpy(ids).cuda(), G)
+    ref_row, ref_counts, first = om.expert_rows(ids, G)
+    assert np.array_equal(row_of.cpu().numpy(), ref_row)
+    assert np.array_equal(counts.cpu().numpy(), ref_counts)
+    assert np.array_equal(m_idx.cpu().numpy(), om.m_indices(ref_counts, first, m_idx.numel()))
+
+
+@pytest.mark.parametrize("G", [1, 2, 3, 4, 5, 31, 32, 33, 127, 128, 129, 1023])
+def test_rows_around_powers_of_two_of_experts(G):
+    ids = choices(700, 6, G, seed=G, stray=0.2)
+    row_of, masked_m, counts = dg.moe_rows_masked(torch.from_numpy(ids).cuda(), G, 50)
+    ref_row, ref_counts, _ = om.expert_rows(ids, G, 50)
+    assert np.array_equal(row_of.cpu().numpy(), ref_row)
+    assert np.array_equal(counts.cpu().numpy(), ref_counts)
+    assert np.array_equal(masked_m.cpu().numpy(), np.minimum(ref_counts, 50))
+
+
 # ---------------------------------------------------- dispatch and quantiser ----
 
 def activations(T, H, dtype, seed):
