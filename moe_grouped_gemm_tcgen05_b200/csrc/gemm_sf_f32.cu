@@ -67,7 +67,7 @@ cudaLaunchConfig_t cluster_config(const Entry& e, unsigned blocks, unsigned clus
 // output tiles leave SMs idle. The choice with the least modelled time, in clocks:
 //   waves x (K blocks of the longest range x clocks of a block + fixed clocks).
 // A block takes ~460 clocks on pairs and ~480 on single CTAs (4096x7168x16384:
-// 482 and 505 us; 4096x4096x7168: 119 and 123). With one m-tile the weights
+// 459-475 and 468-505 us; 4096x4096x7168: 113-119 and 118-125). With one m-tile the weights
 // stream from HBM: ~24 bytes per clock at most on one SM, ~2400 on all (as
 // measured for the block-scaled GEMMs).
 constexpr double kPairBlockClocks = 460.0;

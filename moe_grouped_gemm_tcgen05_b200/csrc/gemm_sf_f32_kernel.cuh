@@ -31,6 +31,16 @@
 //   - Two sets of warps that take every other block with all columns, and swap
 //     halves at the end, need 64 KB for the swap and leave too few stages in
 //     flight: 580 us.
+//   - 16 epilogue warps of 32 columns overlap more but hand a buffer back by twice
+//     as many arrivals (503 us on pairs against 467); products handed over two
+//     blocks at a time halve the waits and gain nothing (465 on pairs, 500 against
+//     480 on single CTAs, where three double stages are too few). The clock falls
+//     under the power limit (~1.5 GHz) as the pipes fill up, which eats such gains.
+// Measured as it stands (graph of calls, rotating operands): 4096x7168x16384 459-475
+// us on pairs (2.0-2.1 PFLOP/s), 468-505 on single CTAs; 4096x4096x7168 113-119 and
+// 118-125 us; one row by 4096x7168 11.3 us; with per-row scales, C and an fp32 D
+// 2112x7168x4096 takes 150-166 us (134 without C, 98 with one scale per 128
+// columns, 70 with a bf16 D and no C as well).
 //
 // CTA = 12 warps (three warpgroups), one CTA per SM, persistent:
 //   warp 0      TMA producer (128-byte swizzle, STAGES-deep ring)
