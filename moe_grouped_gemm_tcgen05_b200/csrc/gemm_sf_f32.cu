@@ -16,7 +16,7 @@ using dg::SfF32Params;
 struct Entry {
     int kind, cg;
     bool rowb;      // B scaled per row
-    int epi;        // 1: C and / or an fp32 D
+    int epi;        // 0: bf16 D, 1: fp32 D, 2: C added
     int b_rows;     // rows of B in one load (the tensor map's box)
     int threads, smem;
     int stages;
@@ -25,7 +25,7 @@ struct Entry {
 
 template <int KIND, int CG, bool ROWB, int EPI>
 Entry entry() {
-    using Cfg = dg::SfF32Config<CG, dg::sched_ints<KIND>(), ROWB>;
+    using Cfg = dg::SfF32Config<CG, dg::sched_ints<KIND>(), ROWB, EPI>;
     return {KIND, CG, ROWB, EPI, Cfg::B_ROWS, dg::SF_F32_THREADS, Cfg::SMEM_BYTES, Cfg::STAGES,
             reinterpret_cast<void*>(&dg::fp8_gemm_sf_f32_kernel<KIND, CG, ROWB, EPI>)};
 }
@@ -33,8 +33,9 @@ Entry entry() {
 const Entry kEntries[] = {
     entry<dg::kDense, 1, false, 0>(), entry<dg::kDense, 2, false, 0>(), entry<dg::kDense, 1, true, 0>(),
     entry<dg::kDense, 2, true, 0>(),  entry<dg::kDense, 1, false, 1>(), entry<dg::kDense, 2, false, 1>(),
-    entry<dg::kDense, 1, true, 1>(),  entry<dg::kDense, 2, true, 1>(),  entry<dg::kContiguous, 1, false, 0>(),
-    entry<dg::kMasked, 1, false, 0>(),
+    entry<dg::kDense, 1, true, 1>(),  entry<dg::kDense, 2, true, 1>(),  entry<dg::kDense, 1, false, 2>(),
+    entry<dg::kDense, 2, false, 2>(), entry<dg::kDense, 1, true, 2>(),  entry<dg::kDense, 2, true, 2>(),
+    entry<dg::kContiguous, 1, false, 0>(), entry<dg::kMasked, 1, false, 0>(),
 };
 constexpr int kNumEntries = sizeof(kEntries) / sizeof(kEntries[0]);
 
@@ -144,7 +145,7 @@ dg_status launch(int kind, SfF32Params& p, const void* a, const void* b, int64_t
     p.sfb_vec4 = p.kb % 4 == 0 && is_aligned(p.sfb32, 16);
     p.wait_limit_ns = dg::host_wait_limit_ns();
     p.test_mode = dg::host_test_mode();
-    const Choice choice = choose(dev, kind, sfb_gran_n == 1, p.c != nullptr || p.out_f32, p.rows, p.n, p.kb);
+    const Choice choice = choose(dev, kind, sfb_gran_n == 1, p.c != nullptr ? 2 : p.out_f32, p.rows, p.n, p.kb);
     if (choice.entry < 0) return DG_ERR_UNSUPPORTED;  // a forced combination that is not built
     const Entry& e = kEntries[choice.entry];
     p.num_n_blocks = (p.n + dg::SF_F32_BN - 1) / dg::SF_F32_BN;

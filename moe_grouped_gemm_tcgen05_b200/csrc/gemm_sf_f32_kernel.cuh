@@ -38,9 +38,9 @@
 //     under the power limit (~1.5 GHz) as the pipes fill up, which eats such gains.
 // Measured as it stands (graph of calls, rotating operands): 4096x7168x16384 459-475
 // us on pairs (2.0-2.1 PFLOP/s), 468-505 on single CTAs; 4096x4096x7168 113-119 and
-// 118-125 us; one row by 4096x7168 11.3 us; with per-row scales, C and an fp32 D
-// 2112x7168x4096 takes 150-166 us (134 without C, 98 with one scale per 128
-// columns, 70 with a bf16 D and no C as well).
+// 118-125 us; one row by 4096x7168 11.3 us; 2112x7168x4096 with a bf16 D, an fp32 D,
+// and C with an fp32 D 66, 73 and 88 us, with per-row scales 101, 120 and 135-139 (the
+// products of two scales per element and block are half of the FMA pipe's work then).
 //
 // CTA = 12 warps (three warpgroups), one CTA per SM, persistent:
 //   warp 0      TMA producer (128-byte swizzle, STAGES-deep ring)
@@ -63,6 +63,8 @@
 //
 // Scheduling, masks and bounded waits are those of gemm_kernel.cuh.
 #pragma once
+
+#include <type_traits>
 
 #include "gemm_kernel.cuh"
 
@@ -119,6 +121,22 @@ __device__ __forceinline__ void tmem_read_done(uint32_t (&r)[N]) {
         asm volatile("" : "+r"(r[h]), "+r"(r[h + 1]), "+r"(r[h + 2]), "+r"(r[h + 3]), "+r"(r[h + 4]), "+r"(r[h + 5]),
                           "+r"(r[h + 6]), "+r"(r[h + 7]), "+r"(r[h + 8]), "+r"(r[h + 9]), "+r"(r[h + 10]),
                           "+r"(r[h + 11]), "+r"(r[h + 12]), "+r"(r[h + 13]), "+r"(r[h + 14]), "+r"(r[h + 15]));
+}
+
+// 16 TMEM lanes x 64 columns into registers, in pairs of columns: register 4 j + 2 u + v of
+// lane l holds row 8 u + l / 4, column 8 j + 2 (l % 4) + v.
+__device__ __forceinline__ void tmem_ld_16x256b_x8(uint32_t taddr, uint32_t* r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]),
+          "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
+          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+          "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]),
+          "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
 }
 
 // Scale loads that stay where they are written: left to itself the compiler moves
@@ -209,8 +227,10 @@ constexpr int SF_F32_BN = 128;                        // columns of a tile
 constexpr int SF_F32_LAUNCH_REGS = 168, SF_F32_EPI_REGS = 208, SF_F32_OTHER_REGS = 88;
 static_assert(SF_F32_OTHER_REGS + 2 * SF_F32_EPI_REGS <= 3 * SF_F32_LAUNCH_REGS, "registers of the launch");
 
-// ROWB: B is scaled per row (sfb_gran_n = 1).
-template <int CG, int SCHED_INTS, bool ROWB>
+// ROWB: B is scaled per row (sfb_gran_n = 1). EPI: D is bf16 (0), fp32 (1), or C is
+// added, of D's type (2). (One kernel for all three lost 10% and more in its main
+// loop, even where C was not read: its registers are assigned with C's in mind.)
+template <int CG, int SCHED_INTS, bool ROWB, int EPI>
 struct SfF32Config {
     static constexpr int BN = SF_F32_BN;
     static constexpr int EW = 8;                      // epilogue warps
@@ -220,12 +240,14 @@ struct SfF32Config {
     static constexpr int B_BYTES = B_ROWS * BK;
     static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;
     static constexpr int NBUF = 512 / BN;             // TMEM buffers of a block product
-    // output staging: 32 rows of 64 bytes per epilogue warp, rows 80 bytes apart (no bank conflicts)
-    static constexpr int STG_ROW = 80;
+    // output staging: 32 rows of 64 bytes per epilogue warp, rows 80 bytes apart (no bank
+    // conflicts). With C the whole of the warp's columns, whose C comes in while the
+    // K loop runs (a stage or two of the ring less).
+    static constexpr int STG_ROW = EPI == 2 ? CW * 4 + 16 : 80;
     static constexpr int STG_BYTES = EW * 32 * STG_ROW;
     // scales of four K-blocks per slot: [4][128 rows] (times B's, when that is one
     // per 128 columns), and with ROWB [4][BN columns]
-    static constexpr int SF_SLOTS = ROWB ? 4 : 2;
+    static constexpr int SF_SLOTS = !ROWB ? 2 : EPI == 2 ? 3 : 4;
     static constexpr int SF_SLOT_FLOATS = 4 * BM + (ROWB ? 4 * BN : 0);
     static constexpr int SF_BYTES = SF_SLOTS * SF_SLOT_FLOATS * 4;
     static constexpr int SCHED_BYTES = SCHED_INTS * 4;
@@ -248,11 +270,23 @@ struct StoreRows {
     uint32_t rows;
 };
 
-// CW columns of a warp's 32 rows, from registers (lane = row) to D through the
-// warp's staging rows, 64 bytes of every row at a time: written back, four
+// `bytes` (a multiple of 16, on 16-byte boundaries) to shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+// Where a lane's sums are in its warp's 32 rows x CW columns. One scale of B for
+// all columns: lane = row, sum i = column i. Per-row scales of B: sum
+// 32 h + 4 j + 2 u + v is row 16 h + 8 u + lane / 4, column 8 j + 2 (lane % 4) + v, so
+// that a lane needs 4 scales of A and 16 of B a block instead of 1 and 64. (Read as
+// 16-byte broadcasts, those 64 keep the path from shared memory busy for 512 clocks
+// a block and SM: 2112x7168x4096 with a bf16 D took 116-127 us, with this layout 101.)
+
+// CW columns of a warp's 32 rows, from registers to D through the warp's staging rows, 64 bytes of every row at a time: written back, four
 // lanes take the 64 bytes of a row. (Row-wise 16-byte stores straight from the
 // registers touch 32 rows per instruction and slow the operand loads.)
-template <int CW, int STG_ROW, int EPI>
+template <int CW, int STG_ROW, int EPI, bool ROWB>
 __device__ __forceinline__ void store_rows(const GemmParams& p, const float (&acc)[CW], const StoreRows& to,
                                            int col0, uint8_t* stg, int lane) {
     const int sub = lane >> 2, piece = lane & 3;
@@ -260,8 +294,16 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const float (&ac
 #pragma unroll
         for (int u = 0; u < CW; u += 32) {
             __syncwarp();
+            if constexpr (ROWB) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {  // 16-byte pieces of eight bf16 columns
+                for (int i = 0; i < 32; i += 2) {  // i = 16 h + 4 j + 2 u of these 32 columns
+                    const int h = i >> 4, j = (i >> 2) & 3, a = 32 * h + u / 2 + 4 * j + (i & 2);
+                    *reinterpret_cast<__nv_bfloat162*>(stg + (16 * h + 4 * (i & 2) + sub) * STG_ROW + 16 * j + 4 * piece) =
+                        __floats2bfloat162_rn(acc[a], acc[a + 1]);
+                }
+            }
+#pragma unroll
+            for (int q = 0; !ROWB && q < 4; ++q) {  // 16-byte pieces of eight bf16 columns
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -281,35 +323,42 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const float (&ac
             }
         }
     } else {
-        // C and / or an fp32 D: 16 fp32 columns at a time, all of C's loads issued first
-        float4 c[CW / 16][4];
-        if (p.c != nullptr) {
+        // 16 fp32 columns at a time. C's part of the tile is in staging already, 4 (bf16: 2)
+        // bytes a column; 16 columns of it go to registers and sums take their place (bf16:
+        // stand behind the row's C).
 #pragma unroll
-            for (int u = 0; u < CW; u += 16) {
-                const int col = col0 + u + 4 * piece;
+        for (int u = 0; u < CW; u += 16) {
+            float4 c[4];
+            uint8_t* part = stg;
+            if constexpr (EPI == 2) {
+                if (p.out_f32) {
+                    part += 4 * u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 8 * i + sub;
-                    if (col >= p.n || !((to.rows >> r) & 1u)) continue;
-                    const size_t at = (to.row0 + r) * p.n + col;
-                    if (p.out_f32) {
-                        c[u / 16][i] = *reinterpret_cast<const float4*>(static_cast<const float*>(p.c) + at);
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.c) + at);
-                        c[u / 16][i] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
-                                                   __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
+                    for (int i = 0; i < 4; ++i)
+                        c[i] = *reinterpret_cast<const float4*>(part + (8 * i + sub) * STG_ROW + 16 * piece);
+                } else {
+                    part += 2 * CW;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(stg + (8 * i + sub) * STG_ROW + 2 * u + 8 * piece);
+                        c[i] = make_float4(__uint_as_float(x.x << 16), __uint_as_float(x.x & 0xFFFF0000u),
+                                           __uint_as_float(x.y << 16), __uint_as_float(x.y & 0xFFFF0000u));
                     }
                 }
             }
-        }
-#pragma unroll
-        for (int u = 0; u < CW; u += 16) {
             __syncwarp();
+            if constexpr (ROWB) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int j = u + 4 * q;
-                *reinterpret_cast<float4*>(stg + lane * STG_ROW + 16 * q) =
-                    make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+                for (int i = 0; i < 16; i += 2) {  // i = 8 h + 4 j + 2 u of these 16 columns
+                    const int h = i >> 3, j = (i >> 2) & 1, a = 32 * h + u / 2 + 4 * j + (i & 2);
+                    *reinterpret_cast<float2*>(part + (16 * h + 4 * (i & 2) + sub) * STG_ROW + 32 * j + 8 * piece) =
+                        make_float2(acc[a], acc[a + 1]);
+                }
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    *reinterpret_cast<float4*>(part + lane * STG_ROW + 16 * q) =
+                        make_float4(acc[u + 4 * q], acc[u + 4 * q + 1], acc[u + 4 * q + 2], acc[u + 4 * q + 3]);
             }
             __syncwarp();
             const int col = col0 + u + 4 * piece;
@@ -318,14 +367,14 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const float (&ac
                 const int r = 8 * i + sub;
                 if (col >= p.n || !((to.rows >> r) & 1u)) continue;
                 const size_t at = (to.row0 + r) * p.n + col;
-                float4 v = *reinterpret_cast<const float4*>(stg + r * STG_ROW + 16 * piece);
-                if (p.c != nullptr) {
-                    v.x += c[u / 16][i].x;
-                    v.y += c[u / 16][i].y;
-                    v.z += c[u / 16][i].z;
-                    v.w += c[u / 16][i].w;
+                float4 v = *reinterpret_cast<const float4*>(part + r * STG_ROW + 16 * piece);
+                if constexpr (EPI == 2) {
+                    v.x += c[i].x;
+                    v.y += c[i].y;
+                    v.z += c[i].z;
+                    v.w += c[i].w;
                 }
-                if (p.out_f32) {
+                if (EPI == 1 || p.out_f32) {
                     *reinterpret_cast<float4*>(p.d32 + at) = v;
                 } else {
                     const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y), b1 = __floats2bfloat162_rn(v.z, v.w);
@@ -337,13 +386,11 @@ __device__ __forceinline__ void store_rows(const GemmParams& p, const float (&ac
     }
 }
 
-// EPI 1: the epilogue of C and / or an fp32 D; EPI 0: plain bf16 D. (The plain
-// one, compiled into one kernel with the other, lost 10% in its main loop.)
 template <int KIND, int CG, bool ROWB, int EPI>
 __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(const __grid_constant__ SfF32Params p) {
     static_assert(CG == 1 || KIND == kDense, "CTA pairs are built for the dense form");
     static_assert((!ROWB && EPI == 0) || KIND == kDense, "per-row scales of B, C and an fp32 D: dense form");
-    using Cfg = SfF32Config<CG, sched_ints<KIND>(), ROWB>;
+    using Cfg = SfF32Config<CG, sched_ints<KIND>(), ROWB, EPI>;
     constexpr int BN = Cfg::BN;
     constexpr int CW = Cfg::CW;
     constexpr int NBUF = Cfg::NBUF;
@@ -363,8 +410,9 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
     uint64_t* sfull_bar = tempty_bar + NBUF;     // scales of four K-blocks are in shared memory
     uint64_t* sempty_bar = sfull_bar + Cfg::SF_SLOTS;   // ... and used by every epilogue warp
     uint64_t* drain_bar = sempty_bar + Cfg::SF_SLOTS;         // all MMAs issued for this CTA finished
-    static_assert((2 * STAGES + NBUF + 2 * Cfg::SF_SLOTS + 1) * 8 + 16 <= 512, "barrier space");
-    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(drain_bar + 1);
+    uint64_t* c_bar = drain_bar + 1;             // an epilogue warp's part of C is in staging (EPI 2)
+    static_assert((2 * STAGES + NBUF + 2 * Cfg::SF_SLOTS + 1 + Cfg::EW) * 8 + 16 <= 512, "barrier space");
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(c_bar + Cfg::EW);
     volatile int* s_abort = reinterpret_cast<volatile int*>(s_tmem + 1);
     int* s_prefix = reinterpret_cast<int*>(reinterpret_cast<uint8_t*>(bars) + 512);
     int* s_mm = s_prefix + MAX_MASKED_GROUPS + 4;
@@ -388,6 +436,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             mbar_init(&sempty_bar[i], Cfg::EW);
         }
         mbar_init(drain_bar, SF_F32_ISSUERS);
+        for (int i = 0; i < Cfg::EW; ++i) mbar_init(&c_bar[i], 1);
         *s_abort = 0;
         fence_barrier_init();
     }
@@ -589,20 +638,31 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
         int gcur = 0;
         uint32_t stage = 0, par = 0, buf = 0;
         uint32_t sf_group = 0;       // groups of four K-blocks before this one
+        [[maybe_unused]] uint64_t* const my_c_bar = c_bar + (warp - SF_F32_EPI_WARP0);
+        [[maybe_unused]] uint32_t c_par = 0;
+        [[maybe_unused]] bool c_pending = false;
         bool aborted = false;
         Tile c;
         for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
              t += units) {
             const int mloc = c.m_blk * BM * CG + my_rows + 32 * q + static_cast<int>(lane);
             const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
-            if constexpr (EPI == 1) {
-                // C's part of the tile on its way to L2, a K loop ahead of its use
-                const int col = c.n_blk * BN + grp * CW;
-                if (p.c != nullptr && mloc < p.rows) {
-                    const int size = p.out_f32 ? 4 : 2;
-                    const char* row = static_cast<const char*>(p.c) + (static_cast<size_t>(mloc) * p.n + col) * size;
-                    for (int b = 0; b < CW * size; b += 128)
-                        if (col + b / size < p.n) asm volatile("prefetch.global.L2 [%0];" ::"l"(row + b));
+            if constexpr (EPI == 2) {
+                // C's part of the tile, a K loop ahead of its use: a row per lane
+                if (!split) {
+                    const int col0 = c.n_blk * BN + grp * CW, size = p.out_f32 ? 4 : 2;
+                    const int bytes = max(0, min(CW, p.n - col0)) * size;  // N % 8 == 0: whole 16 bytes
+                    const bool has = mloc < p.rows && bytes > 0;
+                    const uint32_t lanes = __ballot_sync(0xffffffffu, has);
+                    fence_proxy_async_smem();  // the last tile's accesses to staging precede the copies
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_expect_tx(my_c_bar, static_cast<uint32_t>(__popc(lanes) * bytes));
+                    __syncwarp();
+                    if (has)
+                        bulk_load(stg + lane * Cfg::STG_ROW,
+                                  static_cast<const char*>(p.c) + (static_cast<size_t>(mloc) * p.n + col0) * size,
+                                  static_cast<uint32_t>(bytes), my_c_bar);
+                    c_pending = true;
                 }
             }
             float acc[CW];
@@ -613,12 +673,15 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             for (int kb = 4 * c.kg0; kb < kb1; kb += 4) {
                 const uint32_t slot = sf_group % Cfg::SF_SLOTS;
                 if (!wait_block(&sfull_bar[slot], (sf_group / Cfg::SF_SLOTS) & 1u, p, s_abort)) { aborted = true; break; }
-                const float* sf = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 32 * q + lane;
-                [[maybe_unused]] const float* sfb_cols = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 4 * BM + grp * CW;
+                const float* sf = smem_sf + slot * Cfg::SF_SLOT_FLOATS + 32 * q + (ROWB ? lane / 4 : lane);
+                [[maybe_unused]] const float* sfb_cols =
+                    smem_sf + slot * Cfg::SF_SLOT_FLOATS + 4 * BM + grp * CW + 2 * (lane % 4);
                 const int n = min(4, kb1 - kb);
 #pragma unroll 2
                 for (int i = 0; i < n; ++i) {
-                    const float f = sf[i * BM];
+                    float f[ROWB ? 4 : 1];
+#pragma unroll
+                    for (int h = 0; h < (ROWB ? 4 : 1); ++h) f[h] = sf[i * BM + 8 * h];
                     if (!__all_sync(0xffffffffu, mbar_try_wait_addr(done0 + 8 * stage, par)) &&
                         !wait_warp(&done_bar[stage], par, p, s_abort)) {
                         aborted = true;
@@ -629,7 +692,12 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                     // anything is added, and nothing is carried to the next block
                     // but the sums.
                     uint32_t r[CW];
-                    tmem_read<CW>(t_row + buf * BN, r);
+                    if constexpr (ROWB) {
+                        tmem_ld_16x256b_x8(t_row + buf * BN, r);
+                        tmem_ld_16x256b_x8(t_row + (16u << 16) + buf * BN, r + 32);
+                    } else {
+                        tmem_read<CW>(t_row + buf * BN, r);
+                    }
                     tmem_read_done<CW>(r);
                     tc_fence_before();
                     __syncwarp();
@@ -639,19 +707,22 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                     }
                     buf = (buf + 1) % NBUF;
                     if (++stage == STAGES) { stage = 0; par ^= 1u; }
+                    if constexpr (ROWB) {
 #pragma unroll
-                    for (int j = 0; j < CW; j += 4) {
-                        float g[4] = {1.f, 1.f, 1.f, 1.f};
-                        if constexpr (ROWB) {
-                            const float4 g4 = *reinterpret_cast<const float4*>(sfb_cols + i * BN + j);
-                            g[0] = g4.x; g[1] = g4.y; g[2] = g4.z; g[3] = g4.w;
-                        }
+                        for (int j = 0; j < CW / 8; ++j) {
+                            const float2 g = *reinterpret_cast<const float2*>(sfb_cols + i * BN + 8 * j);
 #pragma unroll
-                        for (int e = 0; e < 4; e += 2) {
-                            float x0 = __uint_as_float(r[j + e]), x1 = __uint_as_float(r[j + e + 1]);
-                            if constexpr (ROWB) mul2(x0, x1, x0, x1, g[e], g[e + 1]);
-                            fma2(acc[j + e], acc[j + e + 1], x0, x1, f, f);
+                            for (int h = 0; h < 4; ++h) {
+                                const int a = 32 * (h / 2) + 4 * j + 2 * (h % 2);
+                                float s0, s1;
+                                mul2(s0, s1, g.x, g.y, f[h], f[h]);
+                                fma2(acc[a], acc[a + 1], __uint_as_float(r[a]), __uint_as_float(r[a + 1]), s0, s1);
+                            }
                         }
+                    } else {
+#pragma unroll
+                        for (int a = 0; a < CW; a += 2)
+                            fma2(acc[a], acc[a + 1], __uint_as_float(r[a]), __uint_as_float(r[a + 1]), f[0], f[0]);
                     }
                 }
                 if (aborted) break;
@@ -664,8 +735,13 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             if (kCanSplit && split) {
                 // this K range's partial, for the cluster's sum below (the ring is
                 // idle: every MMA of the one tile has been read back)
-                float* part = reinterpret_cast<float*>(smem_a) + (32 * q + lane) * Cfg::PART_ROW + grp * CW;
-                if (mloc < p.rows) {
+                float* part = reinterpret_cast<float*>(smem_a) + (32 * q + (ROWB ? lane / 4 : lane)) * Cfg::PART_ROW + grp * CW;
+                if constexpr (ROWB) {
+#pragma unroll
+                    for (int a = 0; a < CW; a += 2)
+                        *reinterpret_cast<float2*>(part + (16 * (a / 32) + 8 * (a / 2 % 2)) * Cfg::PART_ROW + 8 * (a / 4 % 8) +
+                                                   2 * (lane % 4)) = make_float2(acc[a], acc[a + 1]);
+                } else if (mloc < p.rows) {
 #pragma unroll
                     for (int i = 0; i < CW; i += 4)
                         *reinterpret_cast<float4*>(part + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
@@ -686,9 +762,16 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 if (in_range && id != c.g) atomicOr(p.status, DEVERR_MIXED_EXPERT_BLOCK);
             }
             to.rows = __ballot_sync(0xffffffffu, valid);
+            if constexpr (EPI == 2) {
+                if (!wait_block(my_c_bar, c_par, p, s_abort)) { aborted = true; break; }
+                c_pending = false;
+                c_par ^= 1u;
+            }
             if (to.rows != 0)
-                store_rows<CW, Cfg::STG_ROW, EPI>(p, acc, to, c.n_blk * BN + grp * CW, stg, static_cast<int>(lane));
+                store_rows<CW, Cfg::STG_ROW, EPI, ROWB>(p, acc, to, c.n_blk * BN + grp * CW, stg, static_cast<int>(lane));
         }
+        // (a wait gave up: the copies land before shared memory goes away)
+        if (EPI == 2 && c_pending) wait_quiet(my_c_bar, c_par, p.wait_limit_ns / 16);
     }
 
     tc_fence_before();
@@ -717,7 +800,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                         sum[0] += lo.x; sum[1] += lo.y; sum[2] += lo.z; sum[3] += lo.w;
                         sum[4] += hi.x; sum[5] += hi.y; sum[6] += hi.z; sum[7] += hi.w;
                     }
-                    cluster_store8<EPI>(p, sum, (static_cast<size_t>(c.m_blk) * BM + row) * p.n + col);
+                    cluster_store8<EPI != 0 ? 1 : 0>(p, sum, (static_cast<size_t>(c.m_blk) * BM + row) * p.n + col);
                 }
             }
         }

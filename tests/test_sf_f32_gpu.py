@@ -136,6 +136,48 @@ def test_accumulate(tile, dtype, in_place):
     check(d, *om.fp8_gemm_nt_sf_f32(*ops, c=f64(c)), K)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("gran", [1, 128])
+@pytest.mark.parametrize("M,N,K,cg", [(1290, 2504, 256, 1), (2590, 2504, 128, 2), (1, 8, 128, 1), (130, 136, 384, 2),
+                                      (95, 200, 640, 1)])
+def test_accumulate_over_many_tiles(M, N, K, cg, gran, dtype):
+    """Several tiles per CTA, whose parts of C follow one another; ragged rows and columns; rows around D stay."""
+    ops = operands(M, N, K, gran=gran, seed=M + gran)
+    dg.set_cta_group(cg)
+    dg.set_splits(1)
+    c = (100 * torch.randn((M, N), generator=torch.Generator().manual_seed(2))).to(dtype)
+    buf = torch.full((M + 64, N), 3.0, dtype=dtype, device="cuda")
+    d = buf[32:32 + M]
+    args = dev(*ops)
+    dg.fp8_gemm_nt_sf_f32(*args, d, c=c.cuda(), sfb_gran_n=gran)
+    check(d, *om.fp8_gemm_nt_sf_f32(*ops, gran=gran, c=f64(c)), K)
+    want = d.clone()
+    d.copy_(c)
+    dg.fp8_gemm_nt_sf_f32(*args, d, c=d, sfb_gran_n=gran)
+    assert torch.equal(d, want)
+    assert (buf[:32] == 3).all() and (buf[32 + M:] == 3).all()
+
+
+@pytest.mark.parametrize("cg", [1, 2])
+def test_a_wait_that_runs_out_with_c_under_way(cg):
+    M, N, K = 300, 512, 2048
+    ops = operands(M, N, K, gran=1, seed=6)
+    args = dev(*ops)
+    c = torch.randn((M, N), generator=torch.Generator().manual_seed(3))
+    d = torch.empty((M, N), device="cuda")
+    dg.set_cta_group(cg)
+    dg.set_splits(1)
+    try:
+        dg.set_test_hooks(1, 200)
+        dg.fp8_gemm_nt_sf_f32(*args, d, c=c.cuda(), sfb_gran_n=1)
+        torch.cuda.synchronize()
+        assert dg.device_error(clear=True) == dg.DEVERR_TIMEOUT
+    finally:
+        dg.set_test_hooks(0, 0)
+    dg.fp8_gemm_nt_sf_f32(*args, d, c=c.cuda(), sfb_gran_n=1)
+    check(d, *om.fp8_gemm_nt_sf_f32(*ops, gran=1, c=f64(c)), K)
+
+
 def test_scales_off_a_16_byte_boundary_and_of_every_size():
     """One element into a buffer: the 16-byte reads of scale rows must not be taken."""
     M, N, K = 140, 264, 1024
