@@ -229,7 +229,9 @@ static_assert(SF_F32_OTHER_REGS + 2 * SF_F32_EPI_REGS <= 3 * SF_F32_LAUNCH_REGS,
 
 // ROWB: B is scaled per row (sfb_gran_n = 1). EPI: D is bf16 (0), fp32 (1), or C is
 // added, of D's type (2). (One kernel for all three lost 10% and more in its main
-// loop, even where C was not read: its registers are assigned with C's in mind.)
+// loop, even where C was not read: its registers are assigned with C's in mind.
+// D's rows stored by bulk copies from staging, too, took 96 us instead of 88 with C,
+// and 78 instead of 73 without: those copies queue with the operands'.)
 template <int CG, int SCHED_INTS, bool ROWB, int EPI>
 struct SfF32Config {
     static constexpr int BN = SF_F32_BN;
