@@ -1,5 +1,7 @@
-"""FP8 block-scaled GEMMs (dense, contiguous and masked M-grouped) and the UE8M0
-pack for B200, as a thin Python binding over libdgb200.so.
+"""FP8 block-scaled GEMMs (dense, contiguous and masked M-grouped; UE8M0 or fp32
+scales), the UE8M0 pack and the calls of a layer of routed experts (routing,
+rows, dispatch, combine and their gradients) for B200, as a thin Python binding
+over libdgb200.so.
 
 Every function here only checks shapes/dtypes/devices on the host and passes
 raw pointers to the C ABI declared in ``include/dgb200.h``; all arithmetic runs
@@ -8,8 +10,8 @@ missing or cannot run on the current device, calls raise.
 
 Tensors are torch tensors used as device memory; work is queued on torch's
 current CUDA stream. No call synchronises or allocates (except the
-convenience allocations of ``pack_ue8m0`` / ``empty_*`` when no output is
-given), so the calls of the method can be captured in a CUDA Graph (no claim
+convenience allocations of ``pack_ue8m0`` / ``empty_*`` / ``moe_*`` when no
+output is given), so the calls of the method can be captured in a CUDA Graph (no claim
 is made for ``fp8_gemm_nt_noalloc``).
 """
 
