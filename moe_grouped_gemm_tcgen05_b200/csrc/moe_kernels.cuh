@@ -884,13 +884,13 @@ __global__ void __launch_bounds__(DISPATCH_THREADS) moe_dispatch_fp8_kernel(cons
     griddep_wait();
     const int lane = static_cast<int>(threadIdx.x & 31u);
     const uint32_t i = blockIdx.x * (DISPATCH_THREADS / 32) + (threadIdx.x >> 5);  // (T * kp < 2^32 - 2^28)
-    const int t = static_cast<int>(i / static_cast<uint32_t>(p.kp));
-    const int word = static_cast<int>(i - static_cast<uint32_t>(t) * static_cast<uint32_t>(p.kp));
-    if (t >= p.tokens) return;
+    const uint32_t t = i / static_cast<uint32_t>(p.kp);
+    if (t >= static_cast<uint32_t>(p.tokens)) return;
+    const int word = static_cast<int>(i - t * static_cast<uint32_t>(p.kp));
     const int block = 4 * word + (lane >> 3);
     const bool there = block < p.kb;
     // the token's rows, one per lane (k <= 32), loaded beside its values
-    int64_t my_row = p.row_of != nullptr ? -1 : t;
+    int64_t my_row = p.row_of != nullptr ? int64_t{-1} : static_cast<int64_t>(t);
     if (p.row_of != nullptr && lane < p.k) my_row = __ldg(p.row_of + static_cast<int64_t>(t) * p.k + lane);
     float v[16];
     if (there) {
