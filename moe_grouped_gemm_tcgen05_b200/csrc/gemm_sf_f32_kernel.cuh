@@ -649,6 +649,32 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
              t += units) {
             const int mloc = c.m_blk * BM * CG + my_rows + 32 * q + static_cast<int>(lane);
             const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
+            const int kb1 = min(4 * c.kg1, p.kb);
+            // A warp without a row that D takes hands everything back unread: 32 experts of
+            // 1-20 rows, 4096x7168, 190 us a call under load instead of 200 (the power limit),
+            // 67-124 rows the same 204. (Boxes of 32 rows of A, as many as the expert has rows
+            // in, took 200 and 225.)
+            if (!__any_sync(0xffffffffu, KIND == kMasked ? mloc < s_mm[c.g] : mloc < p.rows)) {
+                for (int kb = 4 * c.kg0; kb < kb1; kb += 4) {
+                    const uint32_t slot = sf_group % Cfg::SF_SLOTS;
+                    if (!wait_block(&sfull_bar[slot], (sf_group / Cfg::SF_SLOTS) & 1u, p, s_abort)) { aborted = true; break; }
+                    if (lane == 0) mbar_arrive(&sempty_bar[slot]);
+                    ++sf_group;
+                    const int n = min(4, kb1 - kb);
+                    for (int i = 0; i < n; ++i) {
+                        if (!wait_block(&done_bar[stage], par, p, s_abort)) { aborted = true; break; }
+                        if (lane == 0) {
+                            if (CG == 1) mbar_arrive_addr(tempty0 + 8 * buf);
+                            else mbar_arrive_cluster(tempty0 + 8 * buf);
+                        }
+                        buf = (buf + 1) % NBUF;
+                        if (++stage == STAGES) { stage = 0; par ^= 1u; }
+                    }
+                    if (aborted) break;
+                }
+                if (aborted) break;
+                continue;
+            }
             if constexpr (EPI == 2) {
                 // C's part of the tile, a K loop ahead of its use: a row per lane
                 if (!split) {
@@ -671,7 +697,6 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
 #pragma unroll
             for (int i = 0; i < CW; ++i) acc[i] = 0.f;
 
-            const int kb1 = min(4 * c.kg1, p.kb);
             for (int kb = 4 * c.kg0; kb < kb1; kb += 4) {
                 const uint32_t slot = sf_group % Cfg::SF_SLOTS;
                 if (!wait_block(&sfull_bar[slot], (sf_group / Cfg::SF_SLOTS) & 1u, p, s_abort)) { aborted = true; break; }
