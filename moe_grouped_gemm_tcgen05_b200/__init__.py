@@ -543,10 +543,12 @@ def moe_route(logits, k, *, bias=None, score="softmax", n_groups=1, top_groups=1
         _need(bias, "bias", _F32, (E,))
     if ids is None:
         ids = _new((T, max(k, 0)), torch.int32, logits.device)
+    else:
+        _need(ids, "ids", _I32, (T, k))
     if weights is None:
         weights = _new((T, max(k, 0)), torch.float32, logits.device)
-    _need(ids, "ids", _I32, (T, k))
-    _need(weights, "weights", _F32, (T, k))
+    else:
+        _need(weights, "weights", _F32, (T, k))
     stream = _here(logits, bias, ids, weights)
     _check("moe_route",
            load().moe_route(_ptr(logits), int(logits.dtype == torch.float32), _opt(bias), _ptr(ids), _ptr(weights), T, E,
@@ -567,7 +569,8 @@ def moe_route_backward(logits, ids, d_weights, *, score="softmax", renormalize=T
     _need(d_weights, "d_weights", _F32, (T, k))
     if d_logits is None:
         d_logits = torch.empty_like(logits)
-    _need(d_logits, "d_logits", (logits.dtype,), (T, E))
+    else:
+        _need(d_logits, "d_logits", (logits.dtype,), (T, E))
     stream = _here(logits, ids, d_weights, d_logits)
     _check("moe_route_backward",
            load().moe_route_backward(_ptr(logits), int(logits.dtype == torch.float32), _ptr(ids), _ptr(d_weights),
@@ -586,11 +589,13 @@ def _rows_args(ids, G, row_of, counts):
     if ids.dim() != 2:
         raise ValueError(f"ids has shape {tuple(ids.shape)}, expected (T, k)")
     if row_of is None:
-        row_of = torch.empty_like(ids)
+        row_of = _new(ids.shape, torch.int32, ids.device)
+    else:
+        _need(row_of, "row_of", _I32, ids.shape)
     if counts is None:
         counts = _new((max(int(G), 0),), torch.int32, ids.device)
-    _need(row_of, "row_of", _I32, ids.shape)
-    _need(counts, "counts", _I32, (G,))
+    else:
+        _need(counts, "counts", _I32, (G,))
     return row_of, counts
 
 
@@ -602,7 +607,8 @@ def moe_rows_contiguous(ids, G, *, row_of=None, m_indices=None, counts=None):
     T, k = ids.shape
     if m_indices is None:
         m_indices = _new((moe_rows_bound(T, k, G),), torch.int32, ids.device)
-    _need(m_indices, "m_indices", _I32, (m_indices.numel(),))
+    else:
+        _need(m_indices, "m_indices", _I32, (m_indices.numel(),))
     stream = _here(ids, row_of, m_indices, counts)
     _check("moe_rows_contiguous",
            load().moe_rows_contiguous(_ptr(ids), _ptr(row_of), _ptr(m_indices), _ptr(counts), T, k, int(G),
@@ -617,7 +623,8 @@ def moe_rows_masked(ids, G, max_m, *, row_of=None, masked_m=None, counts=None):
     T, k = ids.shape
     if masked_m is None:
         masked_m = _new((G,), torch.int32, ids.device)
-    _need(masked_m, "masked_m", _I32, (G,))
+    else:
+        _need(masked_m, "masked_m", _I32, (G,))
     stream = _here(ids, row_of, masked_m, counts)
     _check("moe_rows_masked",
            load().moe_rows_masked(_ptr(ids), _ptr(row_of), _ptr(masked_m), _ptr(counts), T, k, int(G), int(max_m),
@@ -689,7 +696,8 @@ def moe_combine(y, row_of, weights=None, out=None):
     rows, T, k, H = _combine_args(y, row_of, weights)
     if out is None:
         out = _new((T, H), torch.bfloat16, y.device)
-    _need(out, "out", _BF16, (T, H))
+    else:
+        _need(out, "out", _BF16, (T, H))
     stream = _here(y, row_of, weights, out)
     _check("moe_combine", load().moe_combine(_ptr(y), _ptr(row_of), _opt(weights), _ptr(out), rows, T, k, H, stream))
     return out
@@ -703,7 +711,8 @@ def moe_combine_backward(y, row_of, weights, d_out, d_y, d_weights=None):
     _need(d_y, "d_y", _BF16, y.shape)
     if d_weights is None:
         d_weights = _new((T, k), torch.float32, y.device)
-    _need(d_weights, "d_weights", _F32, (T, k))
+    else:
+        _need(d_weights, "d_weights", _F32, (T, k))
     stream = _here(y, row_of, weights, d_out, d_y, d_weights)
     _check("moe_combine_backward",
            load().moe_combine_backward(_ptr(y), _ptr(row_of), _opt(weights), _ptr(d_out), _ptr(d_y), _ptr(d_weights),
