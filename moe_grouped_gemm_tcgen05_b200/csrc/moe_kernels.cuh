@@ -44,8 +44,8 @@ constexpr float ROUTE_EPS = 1e-20f;    // added to the sum that weights are divi
 // 256 experts hold a few such pairs), and the choice must not depend on the
 // rounding of a fast exponential. So a token where two neighbours of the sorted
 // choice, or the last group that stays and the first that does not, lie within a
-// tolerance (keys: twice the error of the fp32 score, below 1e-6, and the
-// bits that the index took) is ranked again in fp64. Without a bias the
+// tolerance (keys: twice the error of the fp32 score, below 1e-6 of the row's
+// best score, and the bits that the index took) is ranked again in fp64. Without a bias the
 // logits themselves rank like the scores; bf16 logits leave 16 bits free, which
 // hold the whole index, so that no two keys are equal.
 
@@ -101,7 +101,7 @@ __host__ __device__ constexpr int route_index_bits() {
     while ((1 << b) < V) ++b;
     return b;
 }
-// Relative difference (to 1, for keys below 1) under which two fp32 keys may be in the wrong order.
+// Relative difference (to the row's best score, for keys below it) under which two fp32 keys may be in the wrong order.
 template <int V>
 __device__ constexpr float route_tolerance() { return 4e-6f + 2.4e-7f * (1 << route_index_bits<V>()); }
 
@@ -391,6 +391,9 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
             sum = warp_sum(sum);
             inv = sum == 0.f ? 0.f : 1.f / sum;
         }
+        // no score is larger: its error bounds those of the others, and the sum's error
+        // moves all scores by the same factor
+        const float best_score = p.softmax ? inv : 1.f;
         // scores plus bias in fp32
         float s[V];
         if (need_scores) {
@@ -452,7 +455,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
                 const uint32_t hi = __reduce_max_sync(0xffffffffu, !stays && lane < p.groups ? u : 0u);
                 const float least = from_ordered_bits(lo), best_out = from_ordered_bits(hi);
                 // (a difference of infinities is no number, and not close: their order goes by the index)
-                close = least - best_out <= 2.f * route_tolerance<V>() * fmaxf(1.f, fabsf(least));
+                close = least - best_out <= 2.f * route_tolerance<V>() * fmaxf(best_score, fabsf(least));
             }
             if (runs) {
                 if (!((kept >> my_group) & 1u)) {
@@ -492,7 +495,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
                 if (whole_index || below == 0u) return false;
                 if (!by_score) return ((above ^ below) & ~kIndexMask) == 0u;
                 const float a = from_ordered_bits(above & ~kIndexMask), b = from_ordered_bits(below & ~kIndexMask);
-                return a - b <= route_tolerance<V>() * fmaxf(1.f, fmaxf(fabsf(a), fabsf(b)));
+                return a - b <= route_tolerance<V>() * fmaxf(best_score, fmaxf(fabsf(a), fabsf(b)));
             };
             uint32_t next = __shfl_down_sync(0xffffffffu, my_key, 1);
             if (lane == p.k - 1) next = last;
