@@ -156,9 +156,24 @@ __device__ __forceinline__ uint32_t route_rank_groups(const RouteParams& p, Key 
     return __ballot_sync(0xffffffffu, lane < p.groups && rank < p.top_groups);
 }
 
+// A group's score from its best two keys (half their sum: it cannot overflow), and the
+// larger of their sizes (the sum of keys of both signs can be far smaller than its error).
+template <typename Key>
+struct GroupScore {
+    Key score, size;
+    __device__ __forceinline__ GroupScore(const RouteParams& p, Key b1, Key b2)
+        : score(rank_key(p.group_top == 2 ? b1 / 2 + b2 / 2 : b1)), size(p.group_top == 2 ? fmax(fabs(b1), fabs(b2)) : fabs(b1)) {}
+    __device__ __forceinline__ GroupScore from_lane(int l) const {
+        GroupScore g = *this;
+        g.score = __shfl_sync(0xffffffffu, score, l);
+        g.size = __shfl_sync(0xffffffffu, size, l);
+        return g;
+    }
+};
+
 // Score of group `lane` (in lanes below p.groups) from keys in registers in any order.
 template <int V, typename Key>
-__device__ __forceinline__ Key route_group_score(const RouteParams& p, const Key (&key)[V], int lane) {
+__device__ __forceinline__ GroupScore<Key> route_group_score(const RouteParams& p, const Key (&key)[V], int lane) {
     const int size = p.experts / p.groups;
     const int run = size / V;
     if (size % V == 0 && (run & (run - 1)) == 0) {
@@ -174,9 +189,9 @@ __device__ __forceinline__ Key route_group_score(const RouteParams& p, const Key
             b2 = fmax(fmin(b1, c1), fmax(b2, c2));
             b1 = fmax(b1, c1);
         }
-        return __shfl_sync(0xffffffffu, rank_key(p.group_top == 2 ? b1 + b2 : b1), (lane * run) & 31);
+        return GroupScore<Key>(p, b1, b2).from_lane((lane * run) & 31);
     }
-    Key score = static_cast<Key>(-INFINITY);
+    GroupScore<Key> mine(p, static_cast<Key>(-INFINITY), static_cast<Key>(-INFINITY));
     for (int g = 0; g < p.groups; ++g) {
         Key b1 = static_cast<Key>(-INFINITY), b2 = b1;
 #pragma unroll
@@ -193,9 +208,9 @@ __device__ __forceinline__ Key route_group_score(const RouteParams& p, const Key
             b2 = fmax(fmin(b1, c1), fmax(b2, c2));
             b1 = fmax(b1, c1);
         }
-        if (lane == g) score = rank_key(p.group_top == 2 ? b1 + b2 : b1);
+        if (lane == g) mine = GroupScore<Key>(p, b1, b2);
     }
-    return score;
+    return mine;
 }
 
 // Experts of this lane that may be chosen, as a bit mask over its registers.
@@ -285,7 +300,7 @@ __device__ __noinline__ int route_choose64(const RouteParams& p, size_t row, int
         }
     }
     uint32_t kept = 0;
-    if (p.top_groups < p.groups) kept = route_rank_groups(p, route_group_score<V, double>(p, s, lane), lane);
+    if (p.top_groups < p.groups) kept = route_rank_groups(p, route_group_score<V, double>(p, s, lane).score, lane);
     uint32_t alive = route_alive<V>(p, kept, lane);
     int mine = 0;
     for (int j = 0; j < p.k; ++j) {
@@ -430,7 +445,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
         }
         bool close = false;
         if (grouped) {
-            float score;
+            GroupScore<float> group(p, 0.f, 0.f);
             if (runs && by_score) {
                 // each lane's two best, from its sorted keys
                 sort_keys<V>(key);
@@ -441,21 +456,21 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
                     b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));
                     b1 = fmaxf(b1, c1);
                 }
-                score = __shfl_sync(0xffffffffu, rank_key(p.group_top == 2 ? b1 + b2 : b1), (lane * run) & 31);
+                group = GroupScore<float>(p, b1, b2).from_lane((lane * run) & 31);
             } else {
-                score = route_group_score<V, float>(p, s, lane);
+                group = route_group_score<V, float>(p, s, lane);
             }
-            const uint32_t kept = route_rank_groups(p, score, lane);
+            const uint32_t kept = route_rank_groups(p, group.score, lane);
             if (need_scores) {
-                // the worst group that stays against the best that does not (the best
-                // logits of groups are exact, sums and biased scores are not)
-                const uint32_t u = ordered_bits(score);
+                // the least that a group that stays may score against the most that another
+                // may (the best logits of groups are exact, sums and biased scores are not;
+                // infinite scores are, too: their order goes by the index)
+                const float off = isinf(group.score) ? 0.f : 0.5f * route_tolerance<V>() * fmaxf(best_score, group.size);
                 const bool stays = (kept >> lane) & 1u;
-                const uint32_t lo = __reduce_min_sync(0xffffffffu, stays ? u : 0xffffffffu);
-                const uint32_t hi = __reduce_max_sync(0xffffffffu, !stays && lane < p.groups ? u : 0u);
-                const float least = from_ordered_bits(lo), best_out = from_ordered_bits(hi);
-                // (a difference of infinities is no number, and not close: their order goes by the index)
-                close = least - best_out <= 2.f * route_tolerance<V>() * fmaxf(best_score, fabsf(least));
+                const uint32_t lo = __reduce_min_sync(0xffffffffu, stays ? ordered_bits(group.score - off) : 0xffffffffu);
+                const uint32_t hi = __reduce_max_sync(
+                    0xffffffffu, !stays && lane < p.groups ? ordered_bits(group.score + off) : 0u);
+                close = lo <= hi && from_ordered_bits(lo) != -INFINITY;
             }
             if (runs) {
                 if (!((kept >> my_group) & 1u)) {

@@ -117,6 +117,46 @@ def test_route_choices_closer_than_fp32(n, top, gt, E, tied):
     assert np.array_equal(ids.cpu().numpy(), om.route(f64(x), k, f64(bias), "sigmoid", n, top, gt)[0])
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("size,gap", [(0.5, 1e-2), (64.0, 3e-5), (1000.0, 5e-4)])
+@pytest.mark.parametrize("E,n,top", [(64, 8, 4), (256, 8, 3), (60, 4, 2), (512, 32, 7)])
+def test_route_groups_whose_two_best_keys_cancel(E, n, top, size, gap, score):
+    """Group scores are small sums of large keys of both signs: fp32 keys are off by
+    more than the sums are apart, and the 64-bit order must come out."""
+    T, k = 40, top   # the best key of every group that stays
+    r = np.random.default_rng(E + n)
+    per = E // n
+    x = r.standard_normal(E).astype(np.float32)
+    s64 = 1 / (1 + np.exp(-x.astype(np.float64)))
+    if score == "softmax":
+        s64 = np.exp(x.astype(np.float64)) / np.exp(x.astype(np.float64)).sum()
+    bias = np.full(E, -3 * size, np.float32)
+    want = 0.1 + gap * r.permutation(n)
+    for g in range(n):
+        i, j = g * per + r.permutation(per)[:2]
+        bias[i] = size * (1 + r.random())
+        bias[j] = want[g] - (s64[i] + np.float64(bias[i])) - s64[j]
+    xs = np.repeat(x[None], T, 0)
+    xs[1:] += (1e-7 * r.standard_normal((T - 1, E))).astype(np.float32)
+    ids, _ = dg.moe_route(torch.from_numpy(xs).cuda(), k, bias=torch.from_numpy(bias).cuda(), score=score, n_groups=n,
+                          top_groups=top, group_top=2)
+    ref = om.route(xs.astype(np.float64), k, bias.astype(np.float64), score, n, top, 2)[0]
+    assert np.array_equal(ids.cpu().numpy(), ref)
+
+
+@pytest.mark.parametrize("E,n", [(32, 8), (60, 4)])
+def test_route_groups_whose_sum_passes_the_largest_number(E, n):
+    """Keys next to the type's lowest value: two of them have no fp32 sum, and their groups are still ranked."""
+    r = np.random.default_rng(7)
+    per = E // n
+    x = r.standard_normal((6, E)).astype(np.float32)
+    bias = (-3.0e38 - 5e35 * r.permutation(E)).astype(np.float32)
+    bias[:per] = 0.1 * r.standard_normal(per)
+    ids, _ = dg.moe_route(torch.from_numpy(x).cuda(), per + 3, bias=torch.from_numpy(bias).cuda(), score="sigmoid", n_groups=n,
+                          top_groups=2, group_top=2)
+    assert np.array_equal(ids.cpu().numpy(), om.route(x.astype(np.float64), per + 3, bias.astype(np.float64), "sigmoid", n, 2, 2)[0])
+
+
 def test_route_rows_with_nothing_or_with_what_is_not_finite():
     inf, nan = float("inf"), float("nan")
     x = torch.full((6, 40), -inf)
