@@ -477,6 +477,24 @@ def test_captured_and_replayed():
     eager_equals_replay(call, outs, reset)
 
 
+def test_rows_replayed_with_other_choices():
+    T, k, G = 1300, 7, 200
+    batches = [choices(T, k, G, seed=s, stray=0.1) for s in range(3)]
+    ids = torch.from_numpy(batches[0]).cuda()
+    out = dg.moe_rows_contiguous(ids, G)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dg.moe_rows_contiguous(ids, G, row_of=out[0], m_indices=out[1], counts=out[2])
+    for b in batches[1:]:
+        ids.copy_(torch.from_numpy(b))
+        g.replay()
+        ref_row, ref_counts, first = om.expert_rows(b, G)
+        assert np.array_equal(out[0].cpu().numpy(), ref_row) and np.array_equal(out[2].cpu().numpy(), ref_counts)
+        assert np.array_equal(out[1].cpu().numpy(), om.m_indices(ref_counts, first, out[1].numel()))
+    del g
+
+
 def test_other_streams_and_two_calls_at_once():
     T, E, k = 700, 128, 8
     x = [torch.randn((T, E), device="cuda") for _ in range(2)]

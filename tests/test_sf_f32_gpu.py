@@ -321,6 +321,28 @@ def test_captured_and_replayed(M, tile, gran):
     eager_equals_replay(lambda: dg.fp8_gemm_nt_sf_f32(*ops, d, sfb_gran_n=gran), [d], lambda: d.zero_())
 
 
+@pytest.mark.parametrize("gran,cg", [(1, 2), (128, 1)])
+def test_accumulation_in_place_replayed(gran, cg):
+    """Every replay adds once more, as every eager call does."""
+    M, N, K = 700, 1160, 384
+    ops = dev(*operands(M, N, K, gran=gran, seed=8))
+    dg.set_cta_group(cg)
+    dg.set_splits(1)
+    want = torch.ones((M, N), device="cuda")
+    for _ in range(3):
+        dg.fp8_gemm_nt_sf_f32(*ops, want, c=want, sfb_gran_n=gran)
+    d = torch.ones((M, N), device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        dg.fp8_gemm_nt_sf_f32(*ops, d, c=d, sfb_gran_n=gran)
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(d, want)
+    del g
+
+
 def test_two_calls_at_once():
     cases = [dev(*operands(M, 520, 2048, seed=M)) for M in (16, 300)]
     outs = [[torch.empty((c[0].shape[0], 520), dtype=torch.bfloat16, device="cuda") for _ in range(8)] for c in cases]
