@@ -101,6 +101,15 @@ __host__ __device__ constexpr int route_index_bits() {
     while ((1 << b) < V) ++b;
     return b;
 }
+// The value of a key whose lowest bits hold an index, which counts as nothing. Without
+// them the key of -inf (0x007fffff), and 0 ("none left"), would read as a NaN.
+template <int V>
+__device__ __forceinline__ float key_value(uint32_t key) {
+    constexpr uint32_t kIndexMask = (1u << route_index_bits<V>()) - 1u;
+    const uint32_t u = key & ~kIndexMask;
+    return u <= 0x007fffffu ? -INFINITY : from_ordered_bits(u);
+}
+
 // Relative difference (to the row's best score, for keys below it) under which two fp32 keys may be in the wrong order.
 template <int V>
 __device__ constexpr float route_tolerance() { return 4e-6f + 2.4e-7f * (1 << route_index_bits<V>()); }
@@ -449,8 +458,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
             if (runs && by_score) {
                 // each lane's two best, from its sorted keys
                 sort_keys<V>(key);
-                float b1 = key[0] ? from_ordered_bits(key[0] & ~kIndexMask) : -INFINITY, b2 = -INFINITY;
-                if (V > 1 && key[V > 1 ? 1 : 0]) b2 = from_ordered_bits(key[V > 1 ? 1 : 0] & ~kIndexMask);
+                float b1 = key_value<V>(key[0]), b2 = V > 1 ? key_value<V>(key[V > 1 ? 1 : 0]) : -INFINITY;
                 for (int o = 1; o < run; o <<= 1) {
                     const float c1 = __shfl_xor_sync(0xffffffffu, b1, o), c2 = __shfl_xor_sync(0xffffffffu, b2, o);
                     b2 = fmaxf(fminf(b1, c1), fmaxf(b2, c2));

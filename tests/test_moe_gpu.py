@@ -185,6 +185,50 @@ def test_route_rows_with_nothing_or_with_what_is_not_finite():
         assert not torch.isnan(w2[3]).any()   # the NaN expert ranks last and is not chosen
 
 
+def lane_experts(E):
+    """Experts of a lane: the smallest built number that holds E experts in 32 lanes."""
+    return next(v for v in (1, 2, 3, 4, 5, 6, 8, 12, 16, 32) if 32 * v >= E)
+
+
+def check_route_exactly(x, bias, k, score, n, top, gt):
+    T, E = x.shape
+    ids, w = dg.moe_route(x.cuda(), k, bias=bias.cuda(), score=score, n_groups=n, top_groups=top, group_top=gt)
+    ref_ids, ref_w = om.route(f64(x), k, f64(bias), score, n, top, gt)
+    assert np.array_equal(ids.cpu().numpy(), ref_ids)
+    there = ~np.isnan(ref_w)
+    err = np.abs(f64(w) - ref_w)
+    assert np.all(err[there] <= (weight_bound(f64(x), k, score) * np.abs(ref_w))[there])
+    assert np.isnan(f64(w)[~there]).all()
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n,top,gt", [(8, 4, 2), (8, 4, 1)])
+@pytest.mark.parametrize("E", [64, 96, 128, 160, 256, 512])
+@pytest.mark.parametrize("kind", ["lane", "lane and a half", "every other lane", "all but one of a group", "group", "half"])
+def test_route_groups_of_experts_taken_out_by_a_bias_of_minus_infinity(kind, E, n, top, gt, score):
+    """Groups that are runs of lanes, with lanes that hold nothing but -inf beside others."""
+    T, k, V, size = 200, 8, lane_experts(E), E // n
+    g = torch.Generator().manual_seed(E + gt)
+    x = 1.5 * torch.randn((T, E), generator=g)
+    bias = 0.05 * torch.randn((E,), generator=g)
+    out = torch.zeros(E, dtype=torch.bool)
+    if kind == "lane":
+        out[:V] = out[E // 2:E // 2 + V] = True
+    elif kind == "lane and a half":
+        out[:V + (V + 1) // 2] = out[5 * size:5 * size + V + (V + 1) // 2] = True
+    elif kind == "every other lane":
+        out[torch.arange(E) // V % 2 == 1] = True
+    elif kind == "all but one of a group":
+        out[size:2 * size] = out[3 * size:4 * size] = True
+        out[size + 1] = out[4 * size - 1] = False
+    elif kind == "group":
+        out[2 * size:3 * size] = out[7 * size:] = True
+    else:
+        out[torch.randperm(E, generator=g)[:E // 2]] = True
+    bias[out] = -np.inf
+    check_route_exactly(x, bias, k, score, n, top, gt)
+
+
 def test_route_many_tokens():
     """More tokens than warps at once, among them the choices that 16384 random
     tokens leave undecided in fp32."""
