@@ -464,9 +464,10 @@ DG_API dg_status m_grouped_fp8_gemm_nt_masked_sf_f32(const void* a, const float*
  *   group_top : 1 (a group ranks by its best expert) or 2 (by its two best)
  * The choice is made on exact logits (no bias) or on keys good to fp64: where
  * two keys or group scores are too close for fp32 the token is ranked again in
- * fp64. Logits may be -inf (score 0; a row of nothing else has weights 0). A
- * NaN key ranks below every number; a NaN or +inf logit makes the softmax
- * weights of its row NaN. Ids are always k different experts.
+ * fp64. Logits may be -inf (score 0; a row of nothing else has weights 0), and
+ * so may the bias, which takes an expert out unless fewer than k others are
+ * left. A NaN key or group score ranks as -inf; a NaN or +inf logit makes the
+ * softmax weights of its row NaN. Ids are always k different experts.
  * Limits: 1 <= k <= E <= 1024, k <= 32, n_groups <= 32 and a divisor of E,
  * k <= top_groups * E / n_groups, T <= 2^30. Capture safe.
  */

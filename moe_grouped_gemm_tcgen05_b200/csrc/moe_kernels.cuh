@@ -513,12 +513,15 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
             };
             // one more than k: the last choice may be a close one
             for (int j = 0; j <= p.k; ++j) take(j);
-            // logits: equal but for the index's bits; scores: within the tolerance
+            // equal but for the index's bits, infinite keys too (equal ones go by the whole
+            // index); scores: also within the tolerance, which no infinite key has
             auto near = [&](uint32_t above, uint32_t below) {
                 if (whole_index || below == 0u) return false;
-                if (!by_score) return ((above ^ below) & ~kIndexMask) == 0u;
-                const float a = from_ordered_bits(above & ~kIndexMask), b = from_ordered_bits(below & ~kIndexMask);
-                return a - b <= route_tolerance<V>() * fmaxf(best_score, fmaxf(fabsf(a), fabsf(b)));
+                if (((above ^ below) & ~kIndexMask) == 0u) return true;
+                if (!by_score) return false;
+                const float a = key_value<V>(above), b = key_value<V>(below);
+                const float size = fmaxf(best_score, fmaxf(fabsf(a), fabsf(b)));
+                return size < INFINITY && a - b <= route_tolerance<V>() * size;
             };
             uint32_t next = __shfl_down_sync(0xffffffffu, my_key, 1);
             if (lane == p.k - 1) next = last;

@@ -31,14 +31,19 @@ def _best(keys, n):
     return sorted(range(len(keys)), key=lambda i: (-keys[i], i))[:n]
 
 
+def _ranked(v):
+    """Keys and group scores rank as themselves, a NaN as -inf."""
+    return np.where(np.isnan(v), -np.inf, v)
+
+
 def route(logits, k, bias=None, score="softmax", n_groups=1, top_groups=1, group_top=2, renormalize=True, scale=1.0):
     """(ids int32 [T, k], weights float64 [T, k]). Without a bias the experts are
     ranked by their logits, which rank like the scores without their rounding."""
     x = np.asarray(logits, np.float64)
     T, E = x.shape
     s = scores(x, score)
-    key = s if bias is None else s + np.asarray(bias, np.float64)
-    rank = x if bias is None else key
+    key = _ranked(s if bias is None else s + np.asarray(bias, np.float64))
+    rank = _ranked(x) if bias is None else key
     size = E // n_groups
     top = min(group_top, size)
     by_logit = bias is None and top == 1
@@ -48,8 +53,9 @@ def route(logits, k, bias=None, score="softmax", n_groups=1, top_groups=1, group
         if top_groups < n_groups:
             per = []
             for g in groups:
-                mine = (x if by_logit else key)[t, g * size:(g + 1) * size]
-                per.append(sum(sorted(mine, reverse=True)[:top]))
+                mine = (rank if by_logit else key)[t, g * size:(g + 1) * size]
+                with np.errstate(invalid="ignore"):
+                    per.append(float(_ranked(sum(sorted(mine, reverse=True)[:top]))))
             groups = _best(per, top_groups)
         pool = sorted(e for g in groups for e in range(g * size, (g + 1) * size))
         ids[t] = [pool[i] for i in _best([rank[t, e] for e in pool], k)]

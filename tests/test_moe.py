@@ -39,6 +39,19 @@ def test_route_worked_example():
     assert ids.tolist() == [[2]] and w[0, 0] == 0.5
 
 
+def test_route_keys_that_are_not_finite():
+    inf, nan = np.inf, np.nan
+    bias = np.full(8, -inf)
+    bias[5] = 0.0
+    assert om.route(np.zeros((1, 8)), 4, bias, "sigmoid")[0].tolist() == [[5, 0, 1, 2]]
+    assert om.route(np.zeros((1, 8)), 3, [0, 0, inf, 0, 0, inf, 0, inf], "sigmoid")[0].tolist() == [[2, 5, 7]]
+    # a NaN ranks below every number, as an expert and in its group's score
+    x = np.array([[3.0, nan, 0.0, 0.0]])
+    assert om.route(x, 4, np.zeros(4), "sigmoid")[0].tolist() == [[0, 2, 3, 1]]
+    assert om.route(x, 2, np.zeros(4), "sigmoid", 2, 1, 2)[0].tolist() == [[2, 3]]
+    assert om.route(x, 2, np.zeros(4), "softmax")[0].tolist() == [[0, 1]]
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 @pytest.mark.parametrize("k", [1, 3])

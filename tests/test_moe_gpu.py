@@ -229,6 +229,50 @@ def test_route_groups_of_experts_taken_out_by_a_bias_of_minus_infinity(kind, E, 
     check_route_exactly(x, bias, k, score, n, top, gt)
 
 
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n,top,gt", [(1, 1, 1), (8, 4, 2), (8, 4, 1)])
+@pytest.mark.parametrize("E", [64, 128, 160, 256, 512])
+def test_route_fewer_experts_than_choices_left_by_the_bias(E, n, top, gt, score):
+    """Choices among equal infinite keys go to the lowest index, of both signs."""
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn((40, E), generator=g)
+    for alive in ([5], [3, 10], [0, E // 2, E - 1], list(range(7))):
+        bias = torch.full((E,), -np.inf)
+        bias[alive] = 0.0
+        for k in (4, 8):
+            check_route_exactly(x, bias, k, score, n, top, gt)
+    for chosen in ([5, 9, 20], [E - 1, E // 2, 1], list(range(0, E, 5))):
+        bias = 0.1 * torch.randn((E,), generator=g)
+        bias[chosen] = np.inf
+        for k in (2, 8):
+            check_route_exactly(x, bias, k, score, n, top, gt)
+
+
+def test_route_worked_examples_of_infinite_biases():
+    bias = torch.full((256,), -np.inf)
+    bias[5] = 0.0
+    assert dg.moe_route(torch.zeros((1, 256)).cuda(), 4, bias=bias.cuda(), score="sigmoid")[0].tolist() == [[5, 0, 1, 2]]
+    bias = torch.zeros(256)
+    bias[[5, 9, 70]] = np.inf
+    assert dg.moe_route(torch.zeros((1, 256)).cuda(), 2, bias=bias.cuda(), score="sigmoid")[0].tolist() == [[5, 9]]
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n,top,gt", [(1, 1, 1), (8, 4, 2), (8, 4, 1)])
+@pytest.mark.parametrize("E", [40, 64, 160, 256])
+def test_route_logits_that_are_not_finite_under_a_bias(E, n, top, gt, score):
+    """A NaN logit takes its expert (softmax: its row) out, and so does -inf; a lane of them, a group, all."""
+    V, size = lane_experts(E), E // 8
+    g = torch.Generator().manual_seed(E)
+    x = torch.randn((24, E), generator=g)
+    bias = 0.1 * torch.randn((E,), generator=g)
+    for t, value in enumerate([np.nan, -np.inf] * 6):
+        x[2 * t, [slice(0, 1), slice(V, 2 * V), slice(0, V + 1), slice(size, 2 * size), slice(2, E), slice(0, E)][t // 2]] = value
+    if score == "softmax":
+        x[1, 7] = np.inf
+    check_route_exactly(x, bias, 4, score, n, top, gt)
+
+
 def test_route_many_tokens():
     """More tokens than warps at once, among them the choices that 16384 random
     tokens leave undecided in fp32."""
