@@ -139,7 +139,8 @@ struct GemmParams {
 
 // SCHED_INTS: 32-bit words of shared memory for the tile scheduler (masked:
 // clamped masked_m and tile prefix sums; psum_m: the groups' first rows and
-// tile prefix sums; contiguous: expert of every 128-row block; dense: none).
+// tile prefix sums; contiguous: expert of every 128-row block, or the list of
+// blocks that have one; dense: none).
 template <int KIND>
 __host__ __device__ constexpr int sched_ints() {
     return (KIND == kMasked || KIND == kPsum) ? 2 * MAX_MASKED_GROUPS + 8
@@ -256,7 +257,7 @@ __device__ __forceinline__ void sleep_ns(uint64_t ns) {
 
 // ------------------------------------------------------------- scheduling --
 
-// Dense / contiguous: banded raster. Within a band of `raster_group` m-tiles
+// Dense / contiguous: banded raster of m_blocks m-tiles. Within a band of `raster_group` m-tiles
 // the m-tile varies fastest, so CTAs running at the same time share the B tile
 // and a bounded slab of A.
 // The arithmetic is kept free of integer divisions where it can be (each
@@ -264,7 +265,7 @@ __device__ __forceinline__ void sleep_ns(uint64_t ns) {
 // needs none, the band index comes from a float reciprocal corrected to the
 // exact quotient (below 2^20 tiles, where one correction step suffices), and
 // full bands (a power-of-two number of m-tiles) use a shift.
-__device__ __forceinline__ bool raster_tile(const GemmParams& p, int t_unit, Tile& c) {
+__device__ __forceinline__ bool raster_tile(const GemmParams& p, int m_blocks, int t_unit, Tile& c) {
     const int kgc = (p.kb + 3) / 4;  // K groups of four 128-K blocks
     int t = t_unit;                  // output tile; its splits are consecutive work units
     int split = 0;
@@ -276,7 +277,7 @@ __device__ __forceinline__ bool raster_tile(const GemmParams& p, int t_unit, Til
         c.kg0 = split * kgc / p.splits;
         c.kg1 = (split + 1) * kgc / p.splits;
     }
-    const int total = p.num_m_blocks * p.num_n_blocks;
+    const int total = m_blocks * p.num_n_blocks;
     if (t >= total) return false;
     c.base = t;
     c.split = split;
@@ -291,7 +292,7 @@ __device__ __forceinline__ bool raster_tile(const GemmParams& p, int t_unit, Til
     }
     const int local = t - band * band_tiles;
     const int m0 = band * p.raster_group;
-    const int gm = min(p.raster_group, p.num_m_blocks - m0);
+    const int gm = min(p.raster_group, m_blocks - m0);
     if (gm == p.raster_group) {
         c.n_blk = local >> p.raster_shift;
         c.m_blk = m0 + (local & (gm - 1));
@@ -345,7 +346,7 @@ __device__ __forceinline__ int block_expert(const GemmParams& p, int m_blk, uint
     return __reduce_max_sync(0xffffffffu, best);
 }
 
-// block_expert from the shared-memory table built in the kernel's prologue
+// block_expert from the shared-memory table built in the kernel's prologue (pairs)
 // when the blocks fit in it (warp-uniform either way).
 __device__ __forceinline__ int cached_block_expert(const GemmParams& p, const int* s_bexp, int blk, uint32_t lane) {
     const int nblk = (p.rows + BM - 1) / BM;
@@ -353,15 +354,52 @@ __device__ __forceinline__ int cached_block_expert(const GemmParams& p, const in
     return block_expert(p, blk, lane);
 }
 
+// Contiguous form on single CTAs: the blocks that hold an expert's rows are listed
+// in shared memory (when they and their experts fit).
+__device__ __forceinline__ bool blocks_listed(const GemmParams& p) {
+    return p.num_m_blocks <= MAX_CACHED_BLOCKS && p.groups <= (1 << 21);
+}
+
+// A role's cursor before its first tile. Contiguous form on single CTAs: the
+// m-tiles to walk, the listed blocks or all. Tiles and their numbers stay values
+// that the compiler knows to be the same in every lane (a reduction's result is):
+// an epilogue whose tile number came out of a search ran its K loop 4% slower
+// (fp32 scales, 32768 rows by 4096x7168: 955 us, 910 this way).
+template <int KIND, int CG>
+__device__ __forceinline__ int first_cursor(const GemmParams& p, const int* s_prefix) {
+    if constexpr (KIND == kContiguous && CG == 1)
+        return blocks_listed(p) ? __reduce_max_sync(0xffffffffu, s_prefix[MAX_CACHED_BLOCKS]) : p.num_m_blocks;
+    else
+        return 0;
+}
+
+// Block and expert of a tile whose m_blk is its place in the list.
+template <int KIND, int CG>
+__device__ __forceinline__ void place_tile(const GemmParams& p, const int* s_prefix, Tile& c) {
+    if constexpr (KIND == kContiguous && CG == 1) {
+        if (!blocks_listed(p)) return;
+        const int block = __reduce_max_sync(0xffffffffu, s_prefix[c.m_blk]);
+        c.m_blk = block & (MAX_CACHED_BLOCKS - 1);
+        c.g = block / MAX_CACHED_BLOCKS;
+        c.e_own[0] = c.g;
+    }
+}
+
 // Next work unit at or after t (stepping by `units`); false when none is left.
-// Contiguous form on CTA pairs: a pair tile covers two 128-row blocks, which
-// may belong to two experts (segments are 128-row aligned). Tiles are visited
+// Contiguous form: tiles of padding only are not computed (a layout that holds the
+// worst case of a routing ends in such blocks, and experts of other devices
+// leave most of it empty). Single CTAs walk the list of the other blocks; without
+// PLACE a role that needs neither block nor expert yet (or at all) leaves them to
+// place_tile. Past the list's size they search, or, when the roles can do that
+// (EMPTY), take such a tile with no K groups.
+// On CTA pairs a tile covers two 128-row blocks, which may belong to two
+// experts (segments are 128-row aligned). Tiles are visited
 // in two passes over (pair, n-block): pass 0 computes the pair with the first
 // block's expert (the second block's if the first is padding only); pass 1
 // exists only when the second block has another expert, and computes the pair
-// with that one. Rows of the other expert are never written in a pass. Tiles
-// of padding only are skipped. Every role of the CTA takes the same steps.
-template <int KIND, bool NEED_EXPERT, int CG>
+// with that one. Rows of the other expert are never written in a pass.
+// Every role of the CTA takes the same steps.
+template <int KIND, int CG, bool PLACE = true, bool EMPTY = false>
 __device__ __forceinline__ bool next_tile(const GemmParams& p, const int* s_prefix, const int* s_mm, int& t,
                                           int units, int& gcur, Tile& c, uint32_t lane) {
     if constexpr (KIND == kMasked || KIND == kPsum) {
@@ -372,7 +410,7 @@ __device__ __forceinline__ bool next_tile(const GemmParams& p, const int* s_pref
         const int per_pass = p.num_m_blocks * p.num_n_blocks;
         for (; t < 2 * per_pass; t += units) {
             const int pass = t >= per_pass ? 1 : 0;
-            raster_tile(p, t - pass * per_pass, c);
+            raster_tile(p, p.num_m_blocks, t - pass * per_pass, c);
             const int e0 = cached_block_expert(p, s_prefix, 2 * c.m_blk, lane);
             const int e1 = cached_block_expert(p, s_prefix, 2 * c.m_blk + 1, lane);
             c.e_own[0] = e0;
@@ -386,22 +424,33 @@ __device__ __forceinline__ bool next_tile(const GemmParams& p, const int* s_pref
             }
         }
         return false;
-    } else {
-        if (!raster_tile(p, t, c)) return false;
-        if constexpr (KIND == kContiguous && NEED_EXPERT) {
-            c.g = cached_block_expert(p, s_prefix, c.m_blk, lane);
-            c.e_own[0] = c.g;
+    } else if constexpr (KIND == kContiguous) {
+        if (blocks_listed(p)) {
+            if (!raster_tile(p, gcur, t, c)) return false;
+            if constexpr (PLACE) place_tile<KIND, CG>(p, s_prefix, c);
+            return true;
         }
-        return true;
+#pragma unroll 1
+        for (; raster_tile(p, gcur, t, c); t += units) {
+            c.g = block_expert(p, c.m_blk, lane);
+            c.e_own[0] = c.g;
+            if (EMPTY && c.g < 0) c.kg1 = c.g = 0;
+            if (EMPTY || c.g >= 0) return true;
+        }
+        return false;
+    } else {
+        return raster_tile(p, p.num_m_blocks, t, c);
     }
 }
 
 // The tile scheduler's tables in shared memory, from the device metadata.
 // Masked: s_mm[g] = clamped masked_m, s_prefix = tile prefix sums. psum_m:
-// s_mm = the groups' first rows. Contiguous: s_prefix[b] = expert of 128-row
-// block b, when the blocks fit. All THREADS threads of the CTA; the caller
-// synchronises before the tables are read.
-template <int KIND, int THREADS>
+// s_mm = the groups' first rows. Contiguous, when the blocks fit: on pairs
+// s_prefix[b] = expert of 128-row block b; on single CTAs s_prefix[i] = the i-th
+// block that holds an expert's rows, and its expert above that, and
+// s_prefix[MAX_CACHED_BLOCKS] = how many there are. All THREADS threads of the
+// CTA; the caller synchronises before the tables are read.
+template <int KIND, int CG, int THREADS>
 __device__ __forceinline__ void prepare_schedule(const GemmParams& p, int* s_prefix, int* s_mm, uint32_t warp,
                                                  uint32_t lane) {
     if constexpr (KIND == kMasked) {
@@ -499,6 +548,32 @@ __device__ __forceinline__ void prepare_schedule(const GemmParams& p, int* s_pre
                     if (lane == 0 && b0 + u < nblk) s_prefix[b0 + u] = m;
                 }
             }
+            if constexpr (CG == 1) {
+                // the list, in the table's place (an entry moves towards the front only)
+                __syncthreads();
+                if (warp == 0 && blocks_listed(p)) {
+                    int n = 0;
+                    for (int b0 = 0; b0 < nblk; b0 += 256) {
+                        int e[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int b = b0 + 32 * u + static_cast<int>(lane);
+                            e[u] = b < nblk ? s_prefix[b] : -1;
+                        }
+                        __syncwarp();
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const uint32_t live = __ballot_sync(0xffffffffu, e[u] >= 0);
+                            if (e[u] >= 0)
+                                s_prefix[n + __popc(live & ((1u << lane) - 1u))] =
+                                    e[u] * MAX_CACHED_BLOCKS + b0 + 32 * u + static_cast<int>(lane);
+                            n += __popc(live);
+                        }
+                        __syncwarp();
+                    }
+                    if (lane == 0) s_prefix[MAX_CACHED_BLOCKS] = n;
+                }
+            }
         }
     }
 }
@@ -547,7 +622,7 @@ struct ScaleWords {
 
     // B's words of group kg only
     __device__ __forceinline__ void load_b(const GemmParams& p, int n0, int g, int kg, uint32_t lane) {
-        const int32_t* sfb = p.sfb + static_cast<size_t>(KIND == kDense ? 0 : max(g, 0)) * p.nb_sf * p.kp;
+        const int32_t* sfb = p.sfb + static_cast<size_t>(KIND == kDense ? 0 : g) * p.nb_sf * p.kp;
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
@@ -614,7 +689,7 @@ struct ScaleQuads {
         this->n0 = n0;
         this->g = g;
         if (!p.sfb_per_row) return;  // B words are read per group
-        const int32_t* sfb = p.sfb + static_cast<size_t>(KIND == kDense ? 0 : max(g, 0)) * p.nb_sf * p.kp;
+        const int32_t* sfb = p.sfb + static_cast<size_t>(KIND == kDense ? 0 : g) * p.nb_sf * p.kp;
 #pragma unroll
         for (int ch = 0; ch < CH; ++ch) {
 #pragma unroll
@@ -894,7 +969,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
                 // here) plus the bytes the peers' pieces will bring
                 mbar_init(red_free, static_cast<uint32_t>(p.splits - 1));
                 Tile t0;
-                raster_tile(p, static_cast<int>(blockIdx.x), t0);
+                raster_tile(p, p.num_m_blocks, static_cast<int>(blockIdx.x), t0);
                 const int rk = static_cast<int>(cluster_ctarank());
                 for (int q = 0; q < 4; ++q) {
                     mbar_init(&red_full[q], 1);
@@ -922,7 +997,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
     // scheduled right away (it waits for this grid in turn).
     griddep_launch_dependents();
     griddep_wait();
-    prepare_schedule<KIND, NUM_THREADS>(p, s_prefix, s_mm, warp, lane);
+    prepare_schedule<KIND, CG, NUM_THREADS>(p, s_prefix, s_mm, warp, lane);
     tc_fence_before();
     __syncthreads();
     // every CTA's barriers exist before any cross-CTA signal (pairs, cluster split-K)
@@ -939,14 +1014,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
         int stage = 0;
         uint32_t phase = 0;
         int issued = 0;
-        int gcur = 0;
+        int gcur = first_cursor<KIND, CG>(p, s_prefix);
         Tile cur;
         bool aborted = false;
-        for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
+        for (int t = unit; !aborted && next_tile<KIND, CG>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
              t += units) {
             const int a_row = (KIND == kPsum ? cur.row0 : cur.m_blk * BM * CG) + my_rows;
             const int b_row = cur.n_blk * BN + Cfg::B_ROWS * static_cast<int>(rank);
-            const int g = max(cur.g, 0);
+            const int g = cur.g;
             for (int gi = cur.kg0; gi < cur.kg1 && !aborted; ++gi) {
             const int kgrp = rot_group(p, t, gi, kg_count);
             for (int kb = 4 * kgrp; kb < min(4 * kgrp + 4, p.kb); ++kb) {
@@ -1022,9 +1097,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
             // Groups are visited in the MMA warp's order (tile by tile, K groups
             // in order). Two register sets keep the loads of two groups in
             // flight while a third is stored.
-            int ct = unit, cg_cur = 0;
+            int ct = unit, cg_cur = first_cursor<KIND, CG>(p, s_prefix);
             Tile ctile;
-            bool cok = next_tile<KIND, true, CG>(p, s_prefix, s_mm, ct, units, cg_cur, ctile, lane);
+            bool cok = next_tile<KIND, CG>(p, s_prefix, s_mm, ct, units, cg_cur, ctile, lane);
             int ckg = cok ? ctile.kg0 : 0;
             auto load_next = [&](ScaleWords<BN, KIND, CG>& w) -> bool {
                 if (!cok) return false;
@@ -1032,7 +1107,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
                        rot_group(p, ct, ckg, kg_count), lane);
                 if (++ckg == ctile.kg1) {
                     ct += units;
-                    cok = next_tile<KIND, true, CG>(p, s_prefix, s_mm, ct, units, cg_cur, ctile, lane);
+                    cok = next_tile<KIND, CG>(p, s_prefix, s_mm, ct, units, cg_cur, ctile, lane);
                     if (cok) ckg = ctile.kg0;
                 }
                 return true;
@@ -1076,7 +1151,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
                     q_base += 4;
                     if (q_base >= ctile.kg1) {
                         ct += units;
-                        cok = next_tile<KIND, true, CG>(p, s_prefix, s_mm, ct, units, cg_cur, ctile, lane);
+                        cok = next_tile<KIND, CG>(p, s_prefix, s_mm, ct, units, cg_cur, ctile, lane);
                         if (cok) q_base = ctile.kg0 & ~3;
                     }
                     return true;
@@ -1127,7 +1202,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
             uint32_t sf_phase = 0;
             int acc = 0;
             uint32_t acc_phase = 0;
-            int gcur = 0;
+            int gcur = first_cursor<KIND, CG>(p, s_prefix);
             Tile c;
             bool aborted = false;
             // Two sets of scale columns: `sf_cur` feeds the MMAs of the current
@@ -1156,7 +1231,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
                 if (++slot == SF_RING) { slot = 0; sf_phase ^= 1u; }
                 return true;
             };
-            for (int t = unit; !aborted && next_tile<KIND, CG == 2, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+            for (int t = unit; !aborted && next_tile<KIND, CG, false>(p, s_prefix, s_mm, t, units, gcur, c, lane);
                  t += units) {
                 if (!wait_warp(&tempty_bar[acc], acc_phase ^ 1u, p, s_abort)) { aborted = true; break; }
                 tc_fence_after();  // the epilogue's TMEM reads precede the MMAs below
@@ -1243,12 +1318,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1) fp8_block_scaled_gemm_kernel(c
         int acc = 0;
         uint32_t acc_phase = 0;
         uint32_t epi_phase = 0;
-        int gcur = 0;
+        int gcur = first_cursor<KIND, CG>(p, s_prefix);
         int buf = 0;
         [[maybe_unused]] uint32_t c_phase = 0;   // D = C + A.B^T: parity of this warp's C barrier
         bool e_abort = false;                     // a wait inside a chunk's output gave up
         Tile c;
-        for (int t = unit; next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane); t += units) {
+        for (int t = unit; next_tile<KIND, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane); t += units) {
             const int row_coord = c.m_blk * BM * CG + my_rows + 32 * q;
             const int mloc = row_coord + static_cast<int>(lane);
             bool valid;

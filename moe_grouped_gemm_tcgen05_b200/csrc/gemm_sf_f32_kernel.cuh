@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
     }
     griddep_launch_dependents();
     griddep_wait();
-    prepare_schedule<KIND, SF_F32_THREADS>(p, s_prefix, s_mm, warp, lane);
+    prepare_schedule<KIND, CG, SF_F32_THREADS>(p, s_prefix, s_mm, warp, lane);
     tc_fence_before();
     __syncthreads();
     if (CG == 2 || split) cluster_sync();
@@ -466,16 +466,16 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
             // -------------------------------------------------------- TMA producer --
             [[maybe_unused]] uint32_t full_leader0 = 0;
             if constexpr (CG == 2) full_leader0 = mapa_shared(smem_u32(&full_bar[0]), 0);
-            int stage = 0, issued = 0, gcur = 0;
+            int stage = 0, issued = 0, gcur = first_cursor<KIND, CG>(p, s_prefix);
             uint32_t phase = 0;
             Tile cur;
             bool aborted = false;
             const uint32_t tx = static_cast<uint32_t>(CG * (p.a_box_rows * BK + Cfg::B_BYTES));
-            for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
+            for (int t = unit; !aborted && next_tile<KIND, CG, true, true>(p, s_prefix, s_mm, t, units, gcur, cur, lane);
                  t += units) {
                 const int a_row = cur.m_blk * BM * CG + my_rows;
                 const int b_row = cur.n_blk * BN + Cfg::B_ROWS * static_cast<int>(rank);
-                const int g = max(cur.g, 0);
+                const int g = cur.g;
                 const int kb1 = min(4 * cur.kg1, p.kb);
                 for (int kb = 4 * cur.kg0; kb < kb1; ++kb) {
                     if (issued >= STAGES && !wait_warp(&done_bar[stage], phase ^ 1u, p, s_abort)) { aborted = true; break; }
@@ -530,12 +530,12 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 const uint64_t adesc0 = smem_desc_sw128(smem_u32(smem_a));
                 const uint64_t bdesc0 = smem_desc_sw128(smem_u32(smem_b));
                 const uint32_t full0 = smem_u32(full_bar), tempty0 = smem_u32(tempty_bar), done0 = smem_u32(done_bar);
-                int gcur = 0;
+                int gcur = first_cursor<KIND, CG>(p, s_prefix);
                 uint32_t item0 = 0;   // block products before this tile
                 uint32_t stage = mine, par = 0;   // of this warp's next product
                 Tile c;
                 bool aborted = false;
-                for (int t = unit; !aborted && next_tile<KIND, CG == 2, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+                for (int t = unit; !aborted && next_tile<KIND, CG, false, true>(p, s_prefix, s_mm, t, units, gcur, c, lane);
                      t += units) {
                     const uint32_t n = static_cast<uint32_t>(min(4 * c.kg1, p.kb) - 4 * c.kg0);
                     // the products whose number has this warp's parity
@@ -599,15 +599,15 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 ++stored;
                 return true;
             };
-            int gcur = 0;
+            int gcur = first_cursor<KIND, CG>(p, s_prefix);
             Tile c;
             bool aborted = false;
-            for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+            for (int t = unit; !aborted && next_tile<KIND, CG, true, true>(p, s_prefix, s_mm, t, units, gcur, c, lane);
                  t += units) {
                 // rows and columns clamped into the operands (those past them are never stored)
                 const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
                 const int row0 = c.m_blk * BM * CG + my_rows + static_cast<int>(lane);
-                const float* sfb = p.sfb32 + static_cast<size_t>(KIND == kDense ? 0 : max(c.g, 0)) * p.nb_sf * p.kb;
+                const float* sfb = p.sfb32 + static_cast<size_t>(KIND == kDense ? 0 : c.g) * p.nb_sf * p.kb;
                 auto load = [&](int set, int kg) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
         uint8_t* stg = smem_stg + (warp - SF_F32_EPI_WARP0) * 32 * Cfg::STG_ROW;
         const uint32_t done0 = smem_u32(done_bar);
         const uint32_t tempty0 = CG == 1 ? smem_u32(tempty_bar) : mapa_shared(smem_u32(tempty_bar), 0);
-        int gcur = 0;
+        int gcur = first_cursor<KIND, CG>(p, s_prefix);
         uint32_t stage = 0, par = 0, buf = 0;
         uint32_t sf_group = 0;       // groups of four K-blocks before this one
         [[maybe_unused]] uint64_t* const my_c_bar = c_bar + (warp - SF_F32_EPI_WARP0);
@@ -645,16 +645,18 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
         [[maybe_unused]] bool c_pending = false;
         bool aborted = false;
         Tile c;
-        for (int t = unit; !aborted && next_tile<KIND, true, CG>(p, s_prefix, s_mm, t, units, gcur, c, lane);
+        for (int t = unit; !aborted && next_tile<KIND, CG, false, true>(p, s_prefix, s_mm, t, units, gcur, c, lane);
              t += units) {
-            const int mloc = c.m_blk * BM * CG + my_rows + 32 * q + static_cast<int>(lane);
+            // (contiguous: the tile is placed when its sums are complete)
+            int mloc = KIND == kContiguous ? 0 : c.m_blk * BM * CG + my_rows + 32 * q + static_cast<int>(lane);
             const size_t a_base = KIND == kMasked ? static_cast<size_t>(c.g) * p.rows : 0;
             const int kb1 = min(4 * c.kg1, p.kb);
             // A warp without a row that D takes hands everything back unread: 32 experts of
             // 1-20 rows, 4096x7168, 190 us a call under load instead of 200 (the power limit),
             // 67-124 rows the same 204. (Boxes of 32 rows of A, as many as the expert has rows
             // in, took 200 and 225.)
-            if (!__any_sync(0xffffffffu, KIND == kMasked ? mloc < s_mm[c.g] : mloc < p.rows)) {
+            // (Contiguous: only the last block can have such warps.)
+            if (KIND != kContiguous && !__any_sync(0xffffffffu, KIND == kMasked ? mloc < s_mm[c.g] : mloc < p.rows)) {
                 for (int kb = 4 * c.kg0; kb < kb1; kb += 4) {
                     const uint32_t slot = sf_group % Cfg::SF_SLOTS;
                     if (!wait_block(&sfull_bar[slot], (sf_group / Cfg::SF_SLOTS) & 1u, p, s_abort)) { aborted = true; break; }
@@ -775,6 +777,10 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                 }
                 continue;  // one tile per CTA
             }
+            if constexpr (KIND == kContiguous) {
+                place_tile<KIND, CG>(p, s_prefix, c);
+                mloc = c.m_blk * BM + 32 * q + static_cast<int>(lane);
+            }
             bool valid;
             StoreRows to;
             to.row0 = a_base + static_cast<size_t>(mloc - static_cast<int>(lane));
@@ -807,7 +813,7 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
         if (split) {
             cluster_sync();  // every partial of the tile is in its CTA's shared memory
             Tile c;
-            if (raster_tile(p, static_cast<int>(blockIdx.x), c) && *s_abort == 0) {
+            if (raster_tile(p, p.num_m_blocks, static_cast<int>(blockIdx.x), c) && *s_abort == 0) {
                 // CTA r of S adds up the 8-column pieces [r NP / S, (r + 1) NP / S) of every row
                 const int S = p.splits, NP = BN / 8;
                 const int r = static_cast<int>(cluster_ctarank());
