@@ -46,19 +46,19 @@ RouteFn<dg::RouteParams> route_fn(int v) {
     }
 }
 
-template <bool F32>
+template <bool F32, bool EXACT_REST>
 RouteFn<dg::RouteBackwardParams> route_backward_fn(int v) {
     switch (v) {
-        case 1: return dg::moe_route_backward_kernel<1, F32>;
-        case 2: return dg::moe_route_backward_kernel<2, F32>;
-        case 3: return dg::moe_route_backward_kernel<3, F32>;
-        case 4: return dg::moe_route_backward_kernel<4, F32>;
-        case 5: return dg::moe_route_backward_kernel<5, F32>;
-        case 6: return dg::moe_route_backward_kernel<6, F32>;
-        case 8: return dg::moe_route_backward_kernel<8, F32>;
-        case 12: return dg::moe_route_backward_kernel<12, F32>;
-        case 16: return dg::moe_route_backward_kernel<16, F32>;
-        default: return dg::moe_route_backward_kernel<32, F32>;
+        case 1: return dg::moe_route_backward_kernel<1, F32, EXACT_REST>;
+        case 2: return dg::moe_route_backward_kernel<2, F32, EXACT_REST>;
+        case 3: return dg::moe_route_backward_kernel<3, F32, EXACT_REST>;
+        case 4: return dg::moe_route_backward_kernel<4, F32, EXACT_REST>;
+        case 5: return dg::moe_route_backward_kernel<5, F32, EXACT_REST>;
+        case 6: return dg::moe_route_backward_kernel<6, F32, EXACT_REST>;
+        case 8: return dg::moe_route_backward_kernel<8, F32, EXACT_REST>;
+        case 12: return dg::moe_route_backward_kernel<12, F32, EXACT_REST>;
+        case 16: return dg::moe_route_backward_kernel<16, F32, EXACT_REST>;
+        default: return dg::moe_route_backward_kernel<32, F32, EXACT_REST>;
     }
 }
 
@@ -206,7 +206,11 @@ dg_status moe_route_backward(const void* logits, int logits_f32, const int32_t* 
     const int v = lane_experts(E);
     cudaLaunchAttribute attr[2];
     const cudaLaunchConfig_t cfg = dg::host_launch(route_blocks(T, 0), dg::ROUTE_THREADS, 0, stream, attr);
-    return launched(cudaLaunchKernelEx(&cfg, logits_f32 ? route_backward_fn<true>(v) : route_backward_fn<false>(v), p));
+    if (p.softmax && !p.renorm)
+        return launched(cudaLaunchKernelEx(
+            &cfg, logits_f32 ? route_backward_fn<true, true>(v) : route_backward_fn<false, true>(v), p));
+    return launched(cudaLaunchKernelEx(
+        &cfg, logits_f32 ? route_backward_fn<true, false>(v) : route_backward_fn<false, false>(v), p));
 }
 
 int64_t moe_rows_bound(int T, int k, int G) {

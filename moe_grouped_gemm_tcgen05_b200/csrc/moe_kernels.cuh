@@ -562,10 +562,14 @@ __global__ void __launch_bounds__(ROUTE_THREADS, V <= 8 ? 4 : 1) moe_route_kerne
 //   otherwise     ds_j = scale * g_j
 //   sigmoid       dx_j = ds_j s_j (1 - s_j), 0 elsewhere
 //   softmax       dx_i = s_i (ds_i - c),  c = sum_j ds_j s_j (scale * mean(g) * eps / S when renormalised)
-// The differences g_j - g_l keep the digits that g_j - mean(g) would cancel.
+// The differences g_j - g_l keep the digits that g_j - mean(g) would cancel. So do, for a
+// chosen expert of a softmax that is not renormalised, those in
+//   ds_i - c = sum over the chosen j of s_j (ds_i - ds_j) + ds_i * (sum of s over the others)
+// when little is left to the others (ds the sum of an expert's slots).
 // One warp per token; lane j < k holds choice j. Ids outside [0, E) count as
 // not chosen; an expert named twice gets both slots' gradients. 16384 tokens of
-// 256 experts take 7.0 us (33.6 MB: L2 holds them), 8191 of 32 in bf16 4.3 us.
+// 256 experts take 7.0 us (33.6 MB: L2 holds them), 8191 of 32 in bf16 4.3 us; not
+// renormalised, a softmax takes 9.0 us for the former, 12.6 where every row is peaked.
 struct RouteBackwardParams {
     const void* logits;      // [T, E]
     const int32_t* ids;      // [T, k]
@@ -582,8 +586,10 @@ __device__ __forceinline__ void store_logit(void* x, size_t i, float v) {
     else static_cast<__nv_bfloat16*>(x)[i] = __float2bfloat16_rn(v);
 }
 
-template <int V, bool F32>
-__global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(const RouteBackwardParams p) {
+// EXACT_REST: a softmax that is not renormalised. (In one instance with the others its
+// registers cost them 3 to 4%; eight blocks per SM: 32 registers, which V <= 8 holds.)
+template <int V, bool F32, bool EXACT_REST>
+__global__ void __launch_bounds__(ROUTE_THREADS, EXACT_REST && V <= 8 ? 8 : 1) moe_route_backward_kernel(const RouteBackwardParams p) {
     griddep_launch_dependents();
     griddep_wait();
     const int lane = static_cast<int>(threadIdx.x & 31u);
@@ -647,13 +653,36 @@ __global__ void __launch_bounds__(ROUTE_THREADS) moe_route_backward_kernel(const
         const int il = __shfl_sync(0xffffffffu, id, l);
         if (il == id) both += dl;
     }
+    float diff = both - c;
+    if constexpr (EXACT_REST) {
+        // (scores that leave a quarter to the others: |ds_i| and |c| are within 4 times the
+        // sum of the terms' sizes, and nothing cancels)
+        if (warp_sum(sj) > 0.75f) {
+            uint32_t chosen = 0;   // which of this lane's entries of the row are chosen
+            bool first = id >= 0;  // no earlier slot names this lane's expert
+            for (int l = 0; l < p.k; ++l) {
+                const int il = __shfl_sync(0xffffffffu, id, l);
+                if (il == id && l < lane) first = false;
+                if (il >= 0 && (il & 31) == lane) chosen |= 1u << (il >> 5);
+            }
+            float rest = 0.f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) rest += (chosen >> i) & 1u ? 0.f : s[i];
+            diff = both * (warp_sum(rest) * inv);
+            const float sf = first ? sj : 0.f;
+            for (int l = 0; l < p.k; ++l) {
+                const float bl = __shfl_sync(0xffffffffu, both, l), sl = __shfl_sync(0xffffffffu, sf, l);
+                diff += sl * (both - bl);
+            }
+        }
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = 32 * i + lane;
         if (e < p.experts) store_logit<F32>(p.d_logits, row + e, p.softmax ? -c * (s[i] * inv) : 0.f);
     }
     __syncwarp();  // the chosen experts' entries are written again, after the row
-    if (id >= 0) store_logit<F32>(p.d_logits, row + id, p.softmax ? sj * (both - c) : both * sj * not_sj);
+    if (id >= 0) store_logit<F32>(p.d_logits, row + id, p.softmax ? sj * diff : both * sj * not_sj);
 }
 
 // ------------------------------------------------------- rows of the experts ----

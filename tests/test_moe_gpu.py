@@ -311,6 +311,43 @@ def test_route_backward(case):
     assert np.all(err <= bound + 1e-38), (err - bound).max()
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("gap", [4.0, 12.0, 16.0, 24.0])
+@pytest.mark.parametrize("E,k,chosen", [(8, 2, None), (256, 8, None), (20, 3, [4, 4, -1]), (33, 4, [7, 32, 7, 0]), (7, 7, None)])
+def test_softmax_gradient_of_a_peaked_row(E, k, chosen, gap, bf16):
+    """Not renormalised, and one expert far above the rest: its gradient s (ds - sum ds s)
+    is a small difference, which must keep its digits. The expert's slots have the
+    largest gradients of their row and the others' are not negative, so that
+        d = s (sum over the other chosen of s_l (D - D_l) + D (sum of s over those not chosen)),
+    D the sum of an expert's slots, has no term below zero: the bound is relative to
+    the gradient itself. Scores are within a weight's error, three of them meet in a
+    term; D_l carry k u of their sum, at most D; the sums add E/32 + 5 + 2 k levels."""
+    T = 16
+    g = torch.Generator().manual_seed(E + int(gap))
+    x = torch.rand((T, E), generator=g)
+    ids = np.argsort(-f64(x), axis=1)[:, :k].astype(np.int32)
+    if chosen is not None:
+        ids[:] = chosen
+    d = torch.rand((T, k), generator=g)
+    for t in range(T):
+        x[t, ids[t, 0]] += gap
+        d[t] = torch.where(torch.from_numpy(ids[t] == ids[t, 0]), 3.0 + d[t], d[t] / k)
+    x = x.to(torch.bfloat16) if bf16 else x
+    got = f64(dg.moe_route_backward(x.cuda(), torch.from_numpy(ids).cuda(), d.cuda(), renormalize=False, scale=1.5))
+    s, gr = om.scores(f64(x), "softmax"), f64(d)
+    for t in range(T):
+        D = np.zeros(E)
+        for j in range(k):
+            if ids[t, j] >= 0:
+                D[ids[t, j]] += 1.5 * gr[t, j]
+        rest = np.setdiff1d(np.arange(E), ids[t])
+        e = ids[t, 0]
+        want = s[t, e] * ((s[t] * (D[e] - D))[np.setdiff1d(np.arange(E), np.r_[rest, e])].sum() + D[e] * s[t, rest].sum())
+        # (D - D_l >= D / 2: its error of (k + 2) u D is within 2 (k + 2) u of it)
+        rel = 3 * weight_bound(f64(x[t:t + 1]), k, "softmax") + (2 * (k + 2) + E / 32 + 5 + 2 * k + 4) * U + (BF16 if bf16 else 0)
+        assert abs(got[t, e] - want) <= rel * want * (1 + BF16), (t, got[t, e], want)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renorm", [False, True])
 def test_route_backward_against_differences(score, renorm):
