@@ -164,13 +164,14 @@ DG_API dg_status dgb200_set_cta_group(int cta_group);
 DG_API dg_status dgb200_set_splits(int splits);
 
 /*
- * Test hook for the failure path (process-wide). wait_limit_ms bounds every
+ * Test hooks (process-wide). wait_limit_ms bounds every
  * wait inside the GEMM kernels (0 restores the default, 2000 ms). mode 1 makes
  * CTA 0 of each GEMM launch withhold the arrive that publishes its first group
  * of scale words (the *_sf_f32 GEMMs: its first operand load), so a wait runs
  * out: that launch leaves its output incomplete, sets
- * DG_DEVERR_TIMEOUT and returns; the CUDA context stays usable. mode 0 is
- * normal operation.
+ * DG_DEVERR_TIMEOUT and returns; the CUDA context stays usable. mode 2 launches
+ * moe_rows_* as on a device with no place for a cluster of more than 8 CTAs.
+ * mode 0 is normal operation.
  */
 DG_API dg_status dgb200_set_test_hooks(int mode, int wait_limit_ms);
 

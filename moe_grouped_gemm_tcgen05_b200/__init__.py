@@ -222,9 +222,9 @@ def set_splits(splits: int):
 
 
 def set_test_hooks(mode: int = 0, wait_limit_ms: int = 0):
-    """Failure-path test hook: mode 1 makes CTA 0 withhold the arrive of its
-    first group of scale words so that a bounded wait runs out (see
-    include/dgb200.h). mode 0 = normal."""
+    """Test hooks: mode 1 makes CTA 0 withhold the arrive of its first group of
+    scale words so that a bounded wait runs out, mode 2 launches moe_rows_* on
+    clusters of at most 8 CTAs (see include/dgb200.h). mode 0 = normal."""
     _check("dgb200_set_test_hooks", load().dgb200_set_test_hooks(int(mode), int(wait_limit_ms)))
 
 

@@ -236,7 +236,7 @@ dg_status setup_device(int dev, DeviceState& st) {
     void* status = nullptr;
     if (cudaGetSymbolAddress(&status, g_dg_device_status) != cudaSuccess) return DG_ERR_CUDA;
     st.status = static_cast<uint32_t*>(status);
-    const dg_status s = dg::setup_moe();
+    const dg_status s = dg::setup_moe(dev);
     return s != DG_OK ? s : dg::setup_sf_f32(dev, st.sms);
 }
 
@@ -924,7 +924,7 @@ dg_status dgb200_set_splits(int splits) {
 }
 
 dg_status dgb200_set_test_hooks(int mode, int wait_limit_ms) {
-    if (mode < 0 || mode > 1 || wait_limit_ms < 0) return DG_ERR_INVALID_ARG;
+    if (mode < 0 || mode > 2 || wait_limit_ms < 0) return DG_ERR_INVALID_ARG;
     g_test_mode.store(mode);
     g_wait_limit_ns.store(wait_limit_ms == 0 ? dg::DEFAULT_WAIT_LIMIT_NS
                                              : static_cast<uint64_t>(wait_limit_ms) * 1000000ull);

@@ -33,8 +33,9 @@ bool host_log();                // DGB200_LOG
 // current device (gemm_sf_f32.cu); part of the device's set-up.
 dg_status setup_sf_f32(int device, int sms);
 
-// Kernel attributes of the calls around the experts' products (moe.cu).
-dg_status setup_moe();
+// Kernel attributes and cluster size of the calls around the experts' products on
+// the current device (moe.cu).
+dg_status setup_moe(int device);
 
 inline bool is_aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

@@ -79,22 +79,30 @@ unsigned route_blocks(int T, int64_t cap) {
 }
 
 // One cluster for n choices: a single CTA while its warps have little to count,
-// else 16 (65536 choices of 256 experts 9.4 us, with 8 CTAs 12.0).
+// else 16, or as many as the device has a place for (65536 choices of 256
+// experts 9.4 us, with 8 CTAs 12.0).
 constexpr int kRowsOneCta = 4096;
+constexpr int kMaxDevices = 64;
+unsigned g_rows_cluster[kMaxDevices];
 
-dg_status rows_launch(dg::RowsParams& p, void* stream) {
-    dg::HostDevice dev;
-    const dg_status s = dg::host_device(&dev);
-    if (s != DG_OK) return s;
-    const int smem = dg::rows_smem_bytes(p.groups);
-    const unsigned ctas = p.n <= kRowsOneCta ? 1 : dg::ROWS_MAX_CLUSTER;
-    cudaLaunchAttribute attr[2];
+cudaLaunchConfig_t rows_config(unsigned ctas, int smem, void* stream, cudaLaunchAttribute* attr) {
     cudaLaunchConfig_t cfg = dg::host_launch(ctas, dg::ROWS_THREADS, static_cast<size_t>(smem), stream, attr);
     attr[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
     attr[cfg.numAttrs].val.clusterDim.x = ctas;
     attr[cfg.numAttrs].val.clusterDim.y = 1;
     attr[cfg.numAttrs].val.clusterDim.z = 1;
     ++cfg.numAttrs;
+    return cfg;
+}
+
+dg_status rows_launch(dg::RowsParams& p, void* stream) {
+    dg::HostDevice dev;
+    const dg_status s = dg::host_device(&dev);
+    if (s != DG_OK) return s;
+    unsigned ctas = p.n <= kRowsOneCta ? 1 : g_rows_cluster[dev.device];
+    if (dg::host_test_mode() == 2 && ctas > 8) ctas = 8;  // (the hook of a device with no place for more)
+    cudaLaunchAttribute attr[2];
+    const cudaLaunchConfig_t cfg = rows_config(ctas, dg::rows_smem_bytes(p.groups), stream, attr);
     return launched(cudaLaunchKernelEx(&cfg, dg::moe_rows_kernel, p));
 }
 
@@ -148,12 +156,23 @@ constexpr int64_t kMaxChoices = int64_t{1} << 30;
 
 namespace dg {
 
-dg_status setup_moe() {
+dg_status setup_moe(int device) {
+    if (g_rows_cluster[device] != 0) return DG_OK;
     // (one value for every call: calls on several threads share the attribute)
     if (cudaFuncSetAttribute(moe_rows_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              rows_smem_bytes(MOE_MAX_EXPERTS)) != cudaSuccess ||
         cudaFuncSetAttribute(moe_rows_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
         return DG_ERR_CUDA;
+    // the largest cluster that the device can hold (a part of a GPU may lack a place for 16 CTAs)
+    unsigned ctas = ROWS_MAX_CLUSTER;
+    for (; ctas > 1; ctas /= 2) {
+        cudaLaunchAttribute attr[2];
+        const cudaLaunchConfig_t cfg = rows_config(ctas, rows_smem_bytes(MOE_MAX_EXPERTS), nullptr, attr);
+        int places = 0;
+        if (cudaOccupancyMaxActiveClusters(&places, moe_rows_kernel, &cfg) == cudaSuccess && places > 0) break;
+        cudaGetLastError();
+    }
+    g_rows_cluster[device] = ctas;
     return DG_OK;
 }
 

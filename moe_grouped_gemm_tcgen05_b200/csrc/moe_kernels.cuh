@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(ROUTE_THREADS, EXACT_REST && V <= 8 ? 8 : 1) m
 
 constexpr int ROWS_THREADS = 1024;
 constexpr int ROWS_WARPS = ROWS_THREADS / 32;
-constexpr int ROWS_MAX_CLUSTER = 16;  // CTAs of one GPC (148 SMs on 8 GPCs: one has 16 at least)
+constexpr int ROWS_MAX_CLUSTER = 16;  // CTAs, where the device has a place for them
 constexpr int ROWS_BATCH = 4;         // steps of 32 choices that overlap
 
 struct RowsParams {

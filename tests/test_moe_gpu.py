@@ -440,6 +440,22 @@ def test_rows_around_powers_of_two_of_experts(G):
     assert np.array_equal(masked_m.cpu().numpy(), np.minimum(ref_counts, 50))
 
 
+@pytest.mark.parametrize("T,k,G", [(9001, 8, 256), (2100, 32, 1024), (700, 6, 33)])
+def test_rows_on_a_device_without_a_place_for_16_ctas(T, k, G):
+    """The hook stands in for the device: the largest cluster that fits takes the choices."""
+    ids = choices(T, k, G, seed=G, stray=0.1)
+    dev = torch.from_numpy(ids).cuda()
+    want = dg.moe_rows_contiguous(dev, G)
+    try:
+        dg.set_test_hooks(2, 0)
+        got = dg.moe_rows_contiguous(dev, G)
+    finally:
+        dg.set_test_hooks(0, 0)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    ref_row, ref_counts, first = om.expert_rows(ids, G)
+    assert np.array_equal(got[0].cpu().numpy(), ref_row) and np.array_equal(got[2].cpu().numpy(), ref_counts)
+
+
 # ---------------------------------------------------- dispatch and quantiser ----
 
 def activations(T, H, dtype, seed):
