@@ -520,6 +520,13 @@ def _here(*tensors):
     return _stream(device)
 
 
+def _fits(fn, *sizes):
+    """Sizes that a C int holds: ctypes would cut larger ones down to their lowest 32 bits.
+    (Callers ask only where a size has a bit above the lowest 31: 0.4 us a call otherwise.)"""
+    if max(sizes) > 0x7FFFFFFF or min(sizes) < -0x80000000:
+        raise DgError(fn, 3)
+
+
 def _score(score):
     if score not in _SCORES:
         raise ValueError(f"score={score!r}: one of {tuple(_SCORES)}")
@@ -538,7 +545,9 @@ def moe_route(logits, k, *, bias=None, score="softmax", n_groups=1, top_groups=1
     groups of experts, ranked by their group_top (1 or 2) best keys."""
     _need(logits, "logits", _LOGITS)
     T, E = logits.shape
-    k = int(k)
+    k, n_groups, top_groups, group_top = int(k), int(n_groups), int(top_groups), int(group_top)
+    if (T | E | k | n_groups | top_groups | group_top) >> 31:
+        _fits("moe_route", T, E, k, n_groups, top_groups, group_top)
     if bias is not None:
         _need(bias, "bias", _F32, (E,))
     if ids is None:
@@ -552,7 +561,7 @@ def moe_route(logits, k, *, bias=None, score="softmax", n_groups=1, top_groups=1
     stream = _here(logits, bias, ids, weights)
     _check("moe_route",
            load().moe_route(_ptr(logits), int(logits.dtype == torch.float32), _opt(bias), _ptr(ids), _ptr(weights), T, E,
-                            k, _score(score), int(n_groups), int(top_groups), int(group_top), int(bool(renormalize)),
+                            k, _score(score), n_groups, top_groups, group_top, int(bool(renormalize)),
                             float(scale), stream))
     return ids, weights
 
@@ -566,6 +575,8 @@ def moe_route_backward(logits, ids, d_weights, *, score="softmax", renormalize=T
     if ids.dim() != 2 or ids.shape[0] != T:
         raise ValueError(f"ids has shape {tuple(ids.shape)}, expected ({T}, k)")
     k = ids.shape[1]
+    if (T | E | k) >> 31:
+        _fits("moe_route_backward", T, E, k)
     _need(d_weights, "d_weights", _F32, (T, k))
     if d_logits is None:
         d_logits = torch.empty_like(logits)
@@ -581,19 +592,25 @@ def moe_route_backward(logits, ids, d_weights, *, score="softmax", renormalize=T
 
 def moe_rows_bound(T: int, k: int, G: int) -> int:
     """Rows that T*k choices of G experts can take in whole 128-row blocks, however they fall."""
-    return int(load().moe_rows_bound(int(T), int(k), int(G)))
+    T, k, G = int(T), int(k), int(G)
+    if (T | k | G) >> 31:
+        _fits("moe_rows_bound", T, k, G)
+    return load().moe_rows_bound(T, k, G)
 
 
-def _rows_args(ids, G, row_of, counts):
+def _rows_args(fn, ids, G, max_m, row_of, counts):
     _need(ids, "ids", _I32)
     if ids.dim() != 2:
         raise ValueError(f"ids has shape {tuple(ids.shape)}, expected (T, k)")
+    T, k = ids.shape
+    if (T | k | G | max_m) >> 31:
+        _fits(fn, T, k, G, max_m)
     if row_of is None:
         row_of = _new(ids.shape, torch.int32, ids.device)
     else:
         _need(row_of, "row_of", _I32, ids.shape)
     if counts is None:
-        counts = _new((max(int(G), 0),), torch.int32, ids.device)
+        counts = _new((max(G, 0),), torch.int32, ids.device)
     else:
         _need(counts, "counts", _I32, (G,))
     return row_of, counts
@@ -603,7 +620,8 @@ def moe_rows_contiguous(ids, G, *, row_of=None, m_indices=None, counts=None):
     """Rows of the contiguous layout for the choices ids int32 [T, k] of G experts ->
     (row_of int32 [T, k], m_indices int32 [m_rows], counts int32 [G]); m_rows is
     moe_rows_bound(T, k, G) unless m_indices is given."""
-    row_of, counts = _rows_args(ids, G, row_of, counts)
+    G = int(G)
+    row_of, counts = _rows_args("moe_rows_contiguous", ids, G, 0, row_of, counts)
     T, k = ids.shape
     if m_indices is None:
         m_indices = _new((moe_rows_bound(T, k, G),), torch.int32, ids.device)
@@ -611,7 +629,7 @@ def moe_rows_contiguous(ids, G, *, row_of=None, m_indices=None, counts=None):
         _need(m_indices, "m_indices", _I32, (m_indices.numel(),))
     stream = _here(ids, row_of, m_indices, counts)
     _check("moe_rows_contiguous",
-           load().moe_rows_contiguous(_ptr(ids), _ptr(row_of), _ptr(m_indices), _ptr(counts), T, k, int(G),
+           load().moe_rows_contiguous(_ptr(ids), _ptr(row_of), _ptr(m_indices), _ptr(counts), T, k, G,
                                       m_indices.numel(), stream))
     return row_of, m_indices, counts
 
@@ -619,16 +637,16 @@ def moe_rows_contiguous(ids, G, *, row_of=None, m_indices=None, counts=None):
 def moe_rows_masked(ids, G, max_m, *, row_of=None, masked_m=None, counts=None):
     """Rows of the masked layout [G, max_m] for the choices ids int32 [T, k] ->
     (row_of int32 [T, k], -1 past max_m; masked_m int32 [G]; counts int32 [G])."""
-    row_of, counts = _rows_args(ids, G, row_of, counts)
+    G, max_m = int(G), int(max_m)
+    row_of, counts = _rows_args("moe_rows_masked", ids, G, max_m, row_of, counts)
     T, k = ids.shape
     if masked_m is None:
-        masked_m = _new((G,), torch.int32, ids.device)
+        masked_m = _new((max(G, 0),), torch.int32, ids.device)
     else:
         _need(masked_m, "masked_m", _I32, (G,))
     stream = _here(ids, row_of, masked_m, counts)
     _check("moe_rows_masked",
-           load().moe_rows_masked(_ptr(ids), _ptr(row_of), _ptr(masked_m), _ptr(counts), T, k, int(G), int(max_m),
-                                  stream))
+           load().moe_rows_masked(_ptr(ids), _ptr(row_of), _ptr(masked_m), _ptr(counts), T, k, G, max_m, stream))
     return row_of, masked_m, counts
 
 
@@ -648,6 +666,8 @@ def moe_dispatch_fp8(x, row_of, q, sf):
     _need(row_of, "row_of", _I32)
     if row_of.dim() != 2 or row_of.shape[0] != T:
         raise ValueError(f"row_of has shape {tuple(row_of.shape)}, expected ({T}, k)")
+    if (T | H | row_of.shape[1]) >> 31:
+        _fits("moe_dispatch_fp8", T, H, row_of.shape[1])
     _need(q, "q", _FP8)
     rows = _row_count(q, H, "q")
     _need(sf, "sf", (torch.int32, torch.float32))
@@ -664,6 +684,8 @@ def quantize_fp8_1x128_sf_f32(x, q=None, sf=None):
     """x [rows, K] bf16/fp32 -> (q E4M3 as uint8 [rows, K], sf fp32 [rows, K/128] = amax / 448)."""
     _need(x, "x", _LOGITS)
     rows, K = x.shape
+    if K >> 31:
+        _fits("quantize_fp8_1x128_sf_f32", K)
     if q is None:
         q = _new((rows, K), torch.uint8, x.device)
     if sf is None:
@@ -677,7 +699,7 @@ def quantize_fp8_1x128_sf_f32(x, q=None, sf=None):
     return q, sf
 
 
-def _combine_args(y, row_of, weights):
+def _combine_args(fn, y, row_of, weights):
     _need(y, "y", _BF16)
     if y.dim() not in (2, 3):
         raise ValueError(f"y has shape {tuple(y.shape)}, expected (rows, H) or (G, max_m, H)")
@@ -685,15 +707,18 @@ def _combine_args(y, row_of, weights):
     _need(row_of, "row_of", _I32)
     if row_of.dim() != 2:
         raise ValueError(f"row_of has shape {tuple(row_of.shape)}, expected (T, k)")
+    T, k = row_of.shape
+    if (T | k | H) >> 31:
+        _fits(fn, T, k, H)
     if weights is not None:
         _need(weights, "weights", _F32, row_of.shape)
-    return _row_count(y, H, "y"), *row_of.shape, H
+    return _row_count(y, H, "y"), T, k, H
 
 
 def moe_combine(y, row_of, weights=None, out=None):
     """out [T, H] bf16 = sum over j of weights[t, j] * y[row_of[t, j]] for y [rows, H] or
     [G, max_m, H] bf16; slots with row -1 add nothing; weights None means ones."""
-    rows, T, k, H = _combine_args(y, row_of, weights)
+    rows, T, k, H = _combine_args("moe_combine", y, row_of, weights)
     if out is None:
         out = _new((T, H), torch.bfloat16, y.device)
     else:
@@ -706,7 +731,7 @@ def moe_combine(y, row_of, weights=None, out=None):
 def moe_combine_backward(y, row_of, weights, d_out, d_y, d_weights=None):
     """Gradients of moe_combine: d_y[row_of[t, j]] = weights[t, j] * d_out[t] (other rows are
     left as they were) and d_weights[t, j] = <y[row_of[t, j]], d_out[t]> fp32."""
-    rows, T, k, H = _combine_args(y, row_of, weights)
+    rows, T, k, H = _combine_args("moe_combine_backward", y, row_of, weights)
     _need(d_out, "d_out", _BF16, (T, H))
     _need(d_y, "d_y", _BF16, y.shape)
     if d_weights is None:
@@ -731,6 +756,8 @@ def fp8_gemm_nt_sf_f32(a, sfa, b, sfb, d, c=None, sfb_gran_n: int = BLOCK):
     _need(b, "b", _FP8)
     N = b.shape[0]
     _need(b, "b", _FP8, (N, K))
+    if (M | N | K) >> 31:
+        _fits("fp8_gemm_nt_sf_f32", M, N, K)
     _need(sfa, "sfa", _F32, (M, K // BLOCK))
     _need(sfb, "sfb", _F32, (_sfb_rows(N, sfb_gran_n), K // BLOCK))
     _need(d, "d", (torch.bfloat16, torch.float32), (M, N))
@@ -751,6 +778,8 @@ def m_grouped_fp8_gemm_nt_contiguous_sf_f32(a, sfa, b, sfb, d, m_indices):
     _need(b, "b", _FP8)
     G, N = b.shape[0], b.shape[1]
     _need(b, "b", _FP8, (G, N, K))
+    if (M_total | N | K | G) >> 31:
+        _fits("m_grouped_fp8_gemm_nt_contiguous_sf_f32", M_total, N, K, G)
     _need(sfa, "sfa", _F32, (M_total, K // BLOCK))
     _need(sfb, "sfb", _F32, (G, _sfb_rows(N, BLOCK), K // BLOCK))
     _need(d, "d", _BF16, (M_total, N))
@@ -770,6 +799,8 @@ def m_grouped_fp8_gemm_nt_masked_sf_f32(a, sfa, b, sfb, d, masked_m):
     _need(b, "b", _FP8)
     N = b.shape[1]
     _need(b, "b", _FP8, (G, N, K))
+    if (G | max_m | N | K) >> 31:
+        _fits("m_grouped_fp8_gemm_nt_masked_sf_f32", G, max_m, N, K)
     _need(sfa, "sfa", _F32, (G, max_m, K // BLOCK))
     _need(sfb, "sfb", _F32, (G, _sfb_rows(N, BLOCK), K // BLOCK))
     _need(d, "d", _BF16, (G, max_m, N))

@@ -233,6 +233,18 @@ def test_binding_refusals():
         dg._score("tanh")
 
 
+def test_sizes_past_a_c_int_are_refused(lib):
+    """Not cut down to their lowest 32 bits, which may be a size that the call takes."""
+    for sizes in ((2 ** 31,), (4, 2 ** 32 + 8), (-2 ** 32 + 2, 1)):
+        with pytest.raises(dg.DgError) as e:
+            dg._fits("moe_route", *sizes)
+        assert e.value.status == 3
+    dg._fits("moe_route", 2 ** 31 - 1, 0, -2 ** 31)
+    for sizes in ((2 ** 32 + 1, 1, 1), (1, 2 ** 32 + 1, 1), (1, 1, -2 ** 32 + 1)):
+        with pytest.raises(dg.DgError):
+            dg.moe_rows_bound(*sizes)
+
+
 def test_binding_refuses_another_device(monkeypatch):
     class On:
         def __init__(self, index):

@@ -584,6 +584,30 @@ def test_combine_gradient_against_differences():
         assert f(yy, f64(w)) - base == pytest.approx(f64(d_y)[r, 5], rel=BF16 + 2 * U, abs=1e-9)
 
 
+# ------------------------------------------------------- sizes past a C int ----
+
+def test_sizes_past_a_c_int_are_refused():
+    big = 2 ** 32
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    x = torch.zeros((4, 16), device="cuda")
+    for call in (lambda: dg.moe_rows_masked(ids, 8, big + 4), lambda: dg.moe_rows_masked(ids, big + 8, 4),
+                 lambda: dg.moe_rows_contiguous(ids, big + 8), lambda: dg.moe_route(x, big + 2),
+                 lambda: dg.moe_route(x, 2, n_groups=big + 4), lambda: dg.moe_route(x, 2, n_groups=4, top_groups=big + 2),
+                 lambda: dg.moe_route(x, 2, group_top=big + 1)):
+        with pytest.raises(dg.DgError) as e:
+            call()
+        assert e.value.status == 3
+    wide = torch.empty((1, big + 128), dtype=torch.bfloat16, device="cuda")
+    row = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    for call in (lambda: dg.quantize_fp8_1x128_sf_f32(wide), lambda: dg.moe_combine(wide, row),
+                 lambda: dg.moe_combine_backward(wide, row, None, wide, wide)):
+        with pytest.raises(dg.DgError) as e:
+            call()
+        assert e.value.status == 3
+    del wide
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------- captured, streams, repeats ----
 
 def test_captured_and_replayed():
