@@ -104,14 +104,13 @@ __host__ __device__ constexpr uint32_t idesc_e4m3_f32(uint32_t m, uint32_t n) {
          | ((m >> 4) << 24);     // M >> 4
 }
 
-// Columns of TMEM (32 lanes x N, N a multiple of 16) into registers, and the
+// Columns of TMEM (32 lanes x N, N a multiple of 32) into registers, and the
 // wait for them; naming the registers keeps their uses behind the wait.
 template <int N>
 __device__ __forceinline__ void tmem_read(uint32_t taddr, uint32_t (&r)[N]) {
-    static_assert(N % 16 == 0, "16 columns at a time");
+    static_assert(N % 32 == 0, "32 columns at a time");
 #pragma unroll
-    for (int h = 0; h + 32 <= N; h += 32) tmem_ld_32x32b_x32(taddr + h, r + h);
-    if constexpr (N % 32 != 0) tmem_ld_32x32b_x16(taddr + N - 16, r + N - 16);
+    for (int h = 0; h < N; h += 32) tmem_ld_32x32b_x32(taddr + h, r + h);
 }
 template <int N>
 __device__ __forceinline__ void tmem_read_done(uint32_t (&r)[N]) {
@@ -475,7 +474,6 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                  t += units) {
                 const int a_row = cur.m_blk * BM * CG + my_rows;
                 const int b_row = cur.n_blk * BN + Cfg::B_ROWS * static_cast<int>(rank);
-                const int g = cur.g;
                 const int kb1 = min(4 * cur.kg1, p.kb);
                 for (int kb = 4 * cur.kg0; kb < kb1; ++kb) {
                     if (issued >= STAGES && !wait_warp(&done_bar[stage], phase ^ 1u, p, s_abort)) { aborted = true; break; }
@@ -486,20 +484,16 @@ __global__ void __launch_bounds__(SF_F32_THREADS, 1) fp8_gemm_sf_f32_kernel(cons
                         const int kx = kb * BK;
                         if constexpr (CG == 1) {
                             mbar_arrive_expect_tx(&full_bar[stage], tx);
-                            if constexpr (KIND == kMasked) tma_load_3d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row, g);
+                            if constexpr (KIND == kMasked) tma_load_3d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row, cur.g);
                             else tma_load_2d(a_dst, &p.tma_a, &full_bar[stage], kx, a_row);
+                            if constexpr (KIND == kDense) tma_load_2d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row);
+                            else tma_load_3d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row, cur.g);
                         } else {
                             // both CTAs' loads complete on the leader's barrier
                             if (leader) mbar_arrive_expect_tx(&full_bar[stage], tx);
-                            tma_load_2d_pair(a_dst, &p.tma_a, full_leader0 + 8u * static_cast<uint32_t>(stage), kx, a_row);
-                        }
-                        if constexpr (CG == 1) {
-                            if constexpr (KIND == kDense) tma_load_2d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row);
-                            else tma_load_3d(b_dst, &p.tma_b, &full_bar[stage], kx, b_row, g);
-                        } else {
                             const uint32_t fb = full_leader0 + 8u * static_cast<uint32_t>(stage);
-                            if constexpr (KIND == kDense) tma_load_2d_pair(b_dst, &p.tma_b, fb, kx, b_row);
-                            else tma_load_3d_pair(b_dst, &p.tma_b, fb, kx, b_row, g);
+                            tma_load_2d_pair(a_dst, &p.tma_a, fb, kx, a_row);
+                            tma_load_2d_pair(b_dst, &p.tma_b, fb, kx, b_row);
                         }
                     }
                     __syncwarp();
