@@ -428,7 +428,8 @@ DG_API dg_status quantize_fp8_1x128(const void* x, int x_f32, void* q, int32_t* 
  *         or 1, anything else returns DG_ERR_INVALID_ARG
  *   c, out_f32 : as in fp8_gemm_nt_acc (c may equal d, and must not overlap it otherwise)
  * Every block is accumulated in fp32 by the tensor core, scaled and added in
- * fp32; D is rounded once. Untouched rows, DG_DEVERR_MIXED_EXPERT_BLOCK,
+ * fp32; D is rounded once. The two scales of a block are multiplied first: their
+ * product should be zero or a normal fp32 number. Untouched rows, DG_DEVERR_MIXED_EXPERT_BLOCK,
  * limits, errors, bounded waits and capture safety are those of the calls
  * named (and at most 2^30 rows and columns). quantize_fp8_1x128_sf_f32 makes A and sfa.
  * The gradients of the dense product Y = X . W^T are the same call: dX = dY . W

@@ -68,9 +68,16 @@ cudaLaunchConfig_t cluster_config(const Entry& e, unsigned blocks, unsigned clus
 // output tiles leave SMs idle. The choice with the least modelled time, in clocks:
 //   waves x (K blocks of the longest range x clocks of a block + fixed clocks).
 // A block takes ~460 clocks on pairs and ~480 on single CTAs (4096x7168x16384:
-// 459-475 and 468-505 us; 4096x4096x7168: 113-119 and 118-125). With one m-tile the weights
+// 459-475 and 468-505 us; 4096x4096x7168: 105-119 and 111-125). With one m-tile the weights
 // stream from HBM: ~24 bytes per clock at most on one SM, ~2400 on all (as
-// measured for the block-scaled GEMMs).
+// measured for the block-scaled GEMMs). These are the clocks of the instance with
+// a bf16 D and one scale per 128 columns, used for all: per-row scales take ~700 a
+// block, and C is per tile. What is chosen for those is near the best all the same:
+// per-row scales without C run 1-5% faster on single CTAs (2112x7168x4096 bf16 95.2
+// against 97.1 us on the pairs that are chosen), with C 1% slower (121.7 against
+// 120.1), one scale per 128 columns with C 12% slower (93.2 against 83.2); splits of
+// M <= 128 are within 7% of the best (128x2112x7168, per-row scales, fp32: 5 splits
+// 18.8 us, 4 splits 17.6).
 constexpr double kPairBlockClocks = 460.0;
 constexpr double kBlockClocks = 480.0;
 constexpr double kStreamBytesPerClk = 2400.0;

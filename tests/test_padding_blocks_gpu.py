@@ -130,3 +130,39 @@ def test_more_experts_than_a_list_entry_holds():
             mine = idx == e
             ref, mag = om.fp8_gemm_nt_sf_f32(a[mine], sfa[mine] if form == "fp32 scales" else two[mine], w, np.ones((1, 1), np.float32))
             check(d[torch.from_numpy(mine).cuda()], ref, mag, K)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_replayed_with_padding_elsewhere(form):
+    """The blocks that a captured call skips are those of the m_indices at the replay."""
+    N, K = 264, 384
+    layouts = [[0, 1, 2, -1, -1, -1, -1], [-1] * 7, [-1, 2, -1, 0, 0, -1, 1], [1] * 7]
+    idx, a, sfa, b, sfb = problem(layouts[3], 3, N, K, seed=7)
+    a[a == 0x7F] = 0x30
+    da, dsa, db, dsb = dev(a, sfa, b, sfb)
+    pa, pb = dg.pack_ue8m0(dsa), dg.pack_ue8m0(dsb)
+    m = torch.empty(len(idx), dtype=torch.int32, device="cuda")
+    d = torch.empty((len(idx), N), dtype=torch.bfloat16, device="cuda")
+    dg.set_cta_group({"block-scaled": 1, "block-scaled pairs": 2}.get(form, 0))
+    m.fill_(-1)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        if form == "fp32 scales":
+            dg.m_grouped_fp8_gemm_nt_contiguous_sf_f32(da, dsa, db, dsb, d, m)
+        else:
+            dg.m_grouped_fp8_gemm_nt_contiguous(da, pa, db, pb, d, m)
+    for blocks in layouts:
+        now = np.repeat(np.array(blocks, np.int32), 128)
+        m.copy_(torch.from_numpy(now))
+        fill_sentinel(d)
+        g.replay()
+        torch.cuda.synchronize()
+        assert is_sentinel(d)[now < 0].all()
+        for e in range(3):
+            mine = now == e
+            if mine.any():
+                ref, mag = om.fp8_gemm_nt_sf_f32(a[mine], sfa[mine], b[e], sfb[e])
+                got = d[torch.from_numpy(mine).cuda()]
+                check(got, ref, mag, K) if form == "fp32 scales" else check_fp(bf16_to_f64(got), ref, str(blocks))
+    del g
