@@ -31,11 +31,13 @@ constexpr float ROUTE_EPS = 1e-20f;    // added to the sum that weights are divi
 // One warp per token, expert e = lane * V + i in register i of its lane, so a
 // group is a run of lanes whenever its size is V times a power of two.
 //
-// What bounds it: instructions. A token of 256 experts is 1 KB of fp32 logits, and
-// its choice ~870 warp instructions with the following representation (1824 with
-// keys and indices apart). 16384 such tokens take 30 us (45 with the indices
-// apart; the memory alone needs 2.7), 64 tokens 4.5 us, nearly all of it latency;
-// bf16 logits under softmax take 19 us. A key is an unsigned integer that orders like the fp32 value, with
+// What bounds it: the chain that a token's instructions form, and their number. A
+// token of 256 experts is 1 KB of fp32 logits, and its choice ~900 warp instructions
+// with the following representation (1824 with keys and indices apart). 16384 such
+// tokens take 30 us (45 with the indices apart; the memory alone needs 2.7): 60% of
+// the issue slots are used, and the warps wait for the round before (a reduction, a
+// ballot and a shift each). 64 tokens take 4.3 us, nearly all of it latency;
+// bf16 logits under softmax take 18.5 us. A key is an unsigned integer that orders like the fp32 value, with
 // the complement of the register's index in its lowest bits; a lane's keys are
 // sorted once, a round takes the largest first key of all lanes (one reduction),
 // and its lane moves up.
