@@ -192,8 +192,9 @@ def lane_experts(E):
 
 def check_route_exactly(x, bias, k, score, n, top, gt):
     T, E = x.shape
-    ids, w = dg.moe_route(x.cuda(), k, bias=bias.cuda(), score=score, n_groups=n, top_groups=top, group_top=gt)
-    ref_ids, ref_w = om.route(f64(x), k, f64(bias), score, n, top, gt)
+    ids, w = dg.moe_route(x.cuda(), k, bias=None if bias is None else bias.cuda(), score=score, n_groups=n, top_groups=top,
+                          group_top=gt)
+    ref_ids, ref_w = om.route(f64(x), k, None if bias is None else f64(bias), score, n, top, gt)
     assert np.array_equal(ids.cpu().numpy(), ref_ids)
     there = ~np.isnan(ref_w)
     err = np.abs(f64(w) - ref_w)
@@ -271,6 +272,20 @@ def test_route_logits_that_are_not_finite_under_a_bias(E, n, top, gt, score):
     if score == "softmax":
         x[1, 7] = np.inf
     check_route_exactly(x, bias, 4, score, n, top, gt)
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("n,top,gt", [(1, 1, 1), (8, 4, 2), (8, 4, 1)])
+@pytest.mark.parametrize("E", [40, 64, 160, 256])
+def test_route_logits_that_are_not_finite_without_a_bias(E, n, top, gt, score, bf16):
+    """Lanes, a group and all but a few of the experts at NaN, -inf or +inf: exact ids."""
+    V, size = lane_experts(E), E // 8
+    g = torch.Generator().manual_seed(E + 1)
+    x = torch.randn((18, E), generator=g)
+    for t, value in enumerate([np.nan, -np.inf, np.inf] * 6):
+        x[t, [slice(0, 1), slice(V, 2 * V), slice(0, V + 1), slice(size, 2 * size), slice(2, E), slice(0, E)][t // 3]] = value
+    check_route_exactly(x.to(torch.bfloat16) if bf16 else x, None, 4, score, n, top, gt)
 
 
 def test_route_many_tokens():
